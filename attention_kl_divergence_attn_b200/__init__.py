@@ -14,12 +14,20 @@ Keys may have fewer heads than the queries (grouped key heads: k_t
 ``kv_len`` (int32 [B] on the device) marks the keys at and past each batch
 element's length as padding; either routes the call to the C ABI's
 ``streamkl_fwd_ex`` / ``streamkl_bwd_ex``.
+Serving with a bounded key-value cache (bf16 or fp16, no gradients):
+  streamkl_key_mass(q, k, lse, ...) -> (mass, lse): attention weight of every key
+  streamkl_decode(q, k_pages, v_pages, page_table, seq_len, ...) -> (out, lse):
+    one new token a sequence over a paged cache
+  streamkl_evict(k_pages, v_pages, page_table, seq_len, mass, budget, ...) ->
+    (new_len, mass, pos): keeps the tokens with the largest weight
 The autograd wrapper with temperature scaling is in ``.autograd``
 (``streamkl_loss``).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -80,6 +88,21 @@ def lib():
             L.streamkl_bwd_ex.restype = _I
             L.streamkl_workspace_size_ex.argtypes = [_I] * 10
             L.streamkl_workspace_size_ex.restype = ctypes.c_size_t
+            L.streamkl_key_mass.argtypes = ([_VP] * 4 + [_I] * 7 + [_F, _I] + [_VP] * 2 + [_I, _VP, _I]
+                                            + [_VP, ctypes.c_size_t] * 2 + [_VP])
+            L.streamkl_key_mass.restype = _I
+            L.streamkl_key_mass_scratch_size.argtypes = [_I] * 7
+            L.streamkl_key_mass_scratch_size.restype = ctypes.c_size_t
+            L.streamkl_decode.argtypes = ([_VP] * 6 + [_I] * 7 + [_VP, _I, ctypes.c_longlong, _VP, _F]
+                                          + [_VP] * 4 + [_I] + [_VP, ctypes.c_size_t] * 2 + [_VP])
+            L.streamkl_decode.restype = _I
+            L.streamkl_decode_scratch_size.argtypes = [_I] * 8
+            L.streamkl_decode_scratch_size.restype = ctypes.c_size_t
+            L.streamkl_evict.argtypes = ([_VP] * 4 + [_I] * 5 + [_VP, _I, ctypes.c_longlong] + [_VP] * 4 + [_I] * 3
+                                         + [_VP] * 3 + [_VP, ctypes.c_size_t] * 2 + [_VP])
+            L.streamkl_evict.restype = _I
+            L.streamkl_evict_scratch_size.argtypes = [_I] * 7
+            L.streamkl_evict_scratch_size.restype = ctypes.c_size_t
             L.streamkl_fwd_noalloc.argtypes = ([_VP] * 4 + shape + [_VP] * 4 + [_VP, ctypes.POINTER(ctypes.c_uint)])
             L.streamkl_fwd_noalloc.restype = _I
             L.streamkl_workspace_size.argtypes = [_I] * 7
@@ -357,11 +380,266 @@ def streamkl_loss_reduce(kl, factor, out=None, stream=None):
     return out
 
 
+# ---------------------------------------------------------------- cache operators
+_words: dict = {}
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1}
+
+
+def _status_word(dev):
+    """The cache operators' status word on this device: 256 bytes that are never replaced, so that a
+    captured graph's pointer to them stays good."""
+    w = _words.get(dev.index)
+    if w is None:
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("the first cache operator on a device must run before a graph capture")
+        with torch.cuda.device(dev):
+            w = torch.zeros(_STATUS_BYTES, dtype=torch.uint8, device=dev)
+            torch.cuda.current_stream(dev).synchronize()       # cleared before any stream uses it
+        _words[dev.index] = w
+    return w
+
+
+@functools.lru_cache(maxsize=1024)
+def _scratch_bytes(fn, dev, *args):
+    return int(getattr(lib(), fn)(*args))
+
+
+@functools.lru_cache(maxsize=1024)
+def _strides(s):
+    return (ctypes.c_longlong * len(s))(*s)
+
+
+def _on(dev, stream):
+    """Context that makes the call's device and stream current (nothing when they are already)."""
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError("stream belongs to another device than the tensors")
+        return torch.cuda.stream(stream)
+    if dev.index != torch.cuda.current_device():
+        return torch.cuda.device(dev)
+    return contextlib.nullcontext()
+
+
+def _check_rows(name, t, ndim, like=None):
+    """A CUDA 16-bit tensor whose rows (last dimension) are contiguous and 16-byte aligned."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in _DTYPES or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA bf16 or fp16 tensor")
+    if t.dim() != ndim or (t.stride(-1) != 1 and t.numel() > 0):
+        raise ValueError(f"{name} must have {ndim} dimensions, the last one contiguous")
+    if t.numel() > 0 and (t.data_ptr() % 16 or any(n > 1 and (s % 8 or s <= 0)
+                                                   for n, s in zip(t.shape[:-1], t.stride()))):
+        raise ValueError(f"{name} must have rows on 16-byte boundaries (strides in multiples of 8, not expanded)")
+    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+        raise ValueError(f"{name} must have the type and device of the other tensors")
+
+
+def _check_vec(name, t, dtype, shape, dev):
+    if (not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != dev or t.shape != torch.Size(shape)
+            or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {str(dtype)[6:]} tensor {list(shape)} on the inputs' device")
+
+
+def _check_pages(k_pages, v_pages, page_table, seq_len, like=None):
+    _check_rows("k_pages", k_pages, 4, like)
+    _check_rows("v_pages", v_pages, 4, k_pages)
+    if k_pages.shape != v_pages.shape:
+        raise ValueError("k_pages and v_pages must have one shape [pages, H_k, page_size, d]")
+    if k_pages.shape[1] < 1 or k_pages.shape[2] < 1:
+        raise ValueError("k_pages must have a key head and a slot a page")
+    dev = k_pages.device
+    if (not isinstance(page_table, torch.Tensor) or page_table.dtype != torch.int32 or page_table.device != dev
+            or page_table.dim() != 2 or (page_table.shape[1] > 1 and page_table.stride(1) != 1)):
+        raise ValueError("page_table must be an int32 tensor [B, max_pages] with contiguous rows on the inputs' device")
+    _check_vec("seq_len", seq_len, torch.int32, (page_table.shape[0],), dev)
+    return dev
+
+
+def _overlap(a, b):
+    pa, pb = a.data_ptr(), b.data_ptr()
+    return pa < pb + b.numel() * b.element_size() and pb < pa + a.numel() * a.element_size()
+
+
+def streamkl_key_mass(q, k, lse=None, scale=None, causal=False, *, kv_len=None, out=None, accumulate=False,
+                      stream=None):
+    """Attention weight that every key receives from the query rows: (mass, lse).
+
+    q [B, H, N_Q, d], k [B, H_k, N_K, d] (bf16 or fp16, d in {64, 128}, H_k
+    dividing H; rows contiguous, other strides free).  mass fp32 [B, H_k, N_K]
+    = the column sums of softmax(scale q k^T), summed over each key head's
+    query heads.  ``lse`` fp32 [B, H, N_Q] are the rows' log-sum-exps if they
+    are at hand (lse_t of ``streamkl_fwd`` for the teacher's q and k, same
+    scale, mask and lengths); otherwise they are computed and returned.
+    ``causal`` and ``kv_len`` as in ``streamkl_fwd``; a row without a visible
+    key adds nothing.  ``out`` supplies mass; with ``accumulate`` the call
+    adds to it (the pieces of a long prompt).  Gradients do not flow.
+    """
+    _check_rows("q", q, 4)
+    _check_rows("k", k, 4, q)
+    B, H, N_Q, d = q.shape
+    H_k, N_K = k.shape[1], k.shape[2]
+    if k.shape != (B, H_k, N_K, d):
+        raise ValueError("inconsistent shapes of q and k")
+    if H_k < 1 or H % H_k:
+        raise ValueError("the key heads must divide the query heads")
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out, the sums to add to")
+    dev = q.device
+    kv_len = _check_lengths(kv_len, B, dev)
+    if lse is not None:
+        _check_vec("lse", lse, torch.float32, (B, H, N_Q), dev)
+    if out is not None:
+        _check_vec("out", out, torch.float32, (B, H_k, N_K), dev)
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    given = lse is not None
+    with _on(dev, stream):
+        word = _status_word(dev)
+        mass = torch.empty(B, H_k, N_K, dtype=torch.float32, device=dev) if out is None else out
+        if not given:
+            lse = torch.empty(B, H, N_Q, dtype=torch.float32, device=dev)
+        nbytes = _scratch_bytes("streamkl_key_mass_scratch_size", dev.index, B, H, H_k, N_Q, N_K, d, int(given))
+        scratch = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+        rc = lib().streamkl_key_mass(_ptr(q), _strides(q.stride()[:3]), _ptr(k), _strides(k.stride()[:3]),
+                                     _DTYPES[q.dtype], B, H, H_k, N_Q, N_K, d, scale, int(bool(causal)),
+                                     _ptr(kv_len), _ptr(lse), int(given), _ptr(mass), int(bool(accumulate)),
+                                     _ptr(word), _STATUS_BYTES, _ptr(scratch), nbytes, _stream(None))
+    if rc:
+        raise StreamKLError("streamkl_key_mass", rc)
+    return mass, lse
+
+
+def streamkl_decode(q, k_pages, v_pages, page_table, seq_len, scale=None, *, mass=None, mass_out=None, out=None,
+                    stream=None):
+    """Attention of one new token a sequence over a paged key-value cache: (out, lse).
+
+    q [B, H, d]; k_pages, v_pages [pages, H_k, page_size, d] (bf16 or fp16,
+    rows contiguous, other strides free: a token-major cache is its
+    transposed view); page_table int32 [B, max_pages]; seq_len int32 [B].
+    Slot t of sequence b is slot t % page_size of page page_table[b, t //
+    page_size].  out [B, H, d] has q's type, lse is fp32 [B, H]; a sequence of
+    length 0 gets 0 and -inf.  ``mass`` fp32 [B, H_k, n] accumulates the
+    tokens' weights, summed over each key head's query heads: in place, or
+    into ``mass_out`` (mass itself then stays as it was).  ``out`` may supply
+    the (out, lse) buffers.  Bad lengths and pages are reported by
+    ``streamkl_check``.  Gradients do not flow.
+    """
+    _check_rows("q", q, 3)
+    dev = _check_pages(k_pages, v_pages, page_table, seq_len, q)
+    B, H, d = q.shape
+    pages, H_k, page, dk = k_pages.shape
+    if dk != d or page_table.shape[0] != B:
+        raise ValueError("inconsistent shapes of q, k_pages and page_table")
+    if H % H_k:
+        raise ValueError("the key heads must divide the query heads")
+    cap = 0
+    if mass is not None:
+        cap = mass.shape[-1] if isinstance(mass, torch.Tensor) and mass.dim() == 3 else -1
+        _check_vec("mass", mass, torch.float32, (B, H_k, max(cap, 0)), dev)
+        if mass_out is None:
+            mass_out = mass
+        _check_vec("mass_out", mass_out, torch.float32, (B, H_k, cap), dev)
+        if mass_out.data_ptr() != mass.data_ptr() and _overlap(mass, mass_out):
+            raise ValueError("mass and mass_out must be one tensor or not overlap")
+    elif mass_out is not None:
+        raise ValueError("mass_out needs mass")
+    if out is not None:
+        _check_vec("out[0]", out[0], q.dtype, (B, H, d), dev)
+        _check_vec("out[1]", out[1], torch.float32, (B, H), dev)
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    with _on(dev, stream):
+        word = _status_word(dev)
+        if out is None:
+            o = torch.empty(B, H, d, dtype=q.dtype, device=dev)
+            lse = torch.empty(B, H, dtype=torch.float32, device=dev)
+        else:
+            o, lse = out
+        max_pages = page_table.shape[1]
+        with_mass = int(mass is not None)
+        nbytes = _scratch_bytes("streamkl_decode_scratch_size", dev.index, B, H, H_k, page, max_pages, d, with_mass,
+                                cap)
+        scratch = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        rc = lib().streamkl_decode(_ptr(q), _strides(q.stride()[:2]), _ptr(k_pages), _strides(k_pages.stride()[:3]),
+                                   _ptr(v_pages), _strides(v_pages.stride()[:3]), _DTYPES[q.dtype], B, H, H_k, d,
+                                   pages, page, _ptr(page_table), max_pages, page_table.stride(0), _ptr(seq_len),
+                                   scale, _ptr(o), _ptr(lse), _ptr(mass), _ptr(mass_out), cap, _ptr(word),
+                                   _STATUS_BYTES, _ptr(scratch), nbytes, _stream(None))
+    if rc:
+        raise StreamKLError("streamkl_decode", rc)
+    return o, lse
+
+
+def streamkl_evict(k_pages, v_pages, page_table, seq_len, mass, budget, *, recent=0, pos=None, next_pos=None,
+                   out=None, stream=None):
+    """Keeps min(seq_len, budget) tokens of every (sequence, key head): (new_len, mass, pos).
+
+    The cache is ``streamkl_decode``'s and is changed in place; mass fp32
+    [B, H_k, n] are the accumulated weights.  Kept are the ``recent`` newest
+    tokens (pos >= next_pos - recent; pos int32 [B, H_k, n] holds the position
+    of each slot's token, next_pos int32 [B] the next token's) and those with
+    the largest weight, the lower slot first among equals.  Kept tokens past
+    the new length move into the slots of evicted ones before it; mass and pos
+    are returned in the new order (0 and -1 past new_len), as new tensors or
+    in ``out`` = (new_len, mass, pos), which must not overlap the inputs.  pos
+    is None if none is given.  A sequence that shares pages with another one
+    is left as it is and reported by ``streamkl_check``.
+    """
+    dev = _check_pages(k_pages, v_pages, page_table, seq_len)
+    pages, H_k, page, d = k_pages.shape
+    B, max_pages = page_table.shape
+    budget, recent = int(budget), int(recent)
+    if budget < 0 or recent < 0 or recent > budget:
+        raise ValueError("budget and recent must satisfy 0 <= recent <= budget")
+    budget, recent = min(budget, 0x7fffffff), min(recent, 0x7fffffff)
+    cap = mass.shape[-1] if isinstance(mass, torch.Tensor) and mass.dim() == 3 else 0
+    _check_vec("mass", mass, torch.float32, (B, H_k, cap), dev)
+    if pos is not None:
+        _check_vec("pos", pos, torch.int32, (B, H_k, cap), dev)
+    if next_pos is not None:
+        _check_vec("next_pos", next_pos, torch.int32, (B,), dev)
+    if recent > 0 and (pos is None or next_pos is None):
+        raise ValueError("recent needs pos and next_pos")
+    if k_pages.numel() and k_pages.data_ptr() == v_pages.data_ptr():
+        raise ValueError("k_pages and v_pages must be two tensors")
+    if out is not None:
+        _check_vec("out[0]", out[0], torch.int32, (B,), dev)
+        _check_vec("out[1]", out[1], torch.float32, (B, H_k, cap), dev)
+        if (out[2] is None) != (pos is None):
+            raise ValueError("out[2] goes with pos")
+        if pos is not None:
+            _check_vec("out[2]", out[2], torch.int32, (B, H_k, cap), dev)
+        ins = [t for t in (seq_len, mass, pos, next_pos, page_table) if t is not None]
+        if any(_overlap(o, i) for o in out if o is not None for i in ins):
+            raise ValueError("out must not overlap the inputs")
+    with _on(dev, stream):
+        word = _status_word(dev)
+        if out is None:
+            new_len = torch.empty(B, dtype=torch.int32, device=dev)
+            mass_out = torch.empty_like(mass)
+            pos_out = None if pos is None else torch.empty_like(pos)
+        else:
+            new_len, mass_out, pos_out = out
+        nbytes = _scratch_bytes("streamkl_evict_scratch_size", dev.index, B, H_k, pages, page, max_pages, cap, budget)
+        scratch = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
+        rc = lib().streamkl_evict(_ptr(k_pages), _strides(k_pages.stride()[:3]), _ptr(v_pages),
+                                  _strides(v_pages.stride()[:3]), B, H_k, d, pages, page, _ptr(page_table), max_pages,
+                                  page_table.stride(0), _ptr(seq_len), _ptr(mass), _ptr(pos), _ptr(next_pos), cap,
+                                  budget, recent, _ptr(new_len), _ptr(mass_out), _ptr(pos_out), _ptr(word),
+                                  _STATUS_BYTES, _ptr(scratch), scratch.numel(), _stream(None))
+    if rc:
+        raise StreamKLError("streamkl_evict", rc)
+    return new_len, mass_out, pos_out
+
+
 def streamkl_check(stream=None, device=None) -> int:
     """Synchronises and raises if a kernel gave up on a bounded wait; returns the status word."""
     ws = workspace(device)
-    code = ctypes.c_uint(0)
-    rc = lib().streamkl_check(_ptr(ws), _stream(stream), ctypes.byref(code))
-    if rc:
-        raise StreamKLError("streamkl_check", rc)
-    return code.value
+    codes = []
+    for w in (ws, _words.get(ws.device.index)):
+        if w is None:
+            continue
+        code = ctypes.c_uint(0)
+        rc = lib().streamkl_check(_ptr(w), _stream(stream), ctypes.byref(code))
+        codes.append((rc, code.value))
+    for rc, _ in codes:
+        if rc:
+            raise StreamKLError("streamkl_check", rc)
+    return codes[0][1] | codes[-1][1]

@@ -1,0 +1,493 @@
+// decode.cuh — attention of one new token per sequence over a paged key-value
+// cache, split over the cache's length and joined:
+//     y_t = scale q . k_t  (t < len),  lse = log sum_t exp(y_t),
+//     o   = sum_t exp(y_t - lse) v_t,
+//     mass_out[t] = mass[t] + sum over the group's heads of exp(y_t - lse).
+//
+// Slot t of sequence b lives in page table[b][t / page], slot t % page of it;
+// the pages' strides are the caller's (head-major or token-major pages, or a
+// contiguous cache as one long page a sequence).
+//
+// The work is the cache's bytes (4 d a token and key head, against 4 d flops a
+// byte-pair and query head), so the kernel is a stream of asynchronous copies:
+//  - The lengths are on the device and may differ by orders of magnitude, so
+//    the grid is fixed and every CTA takes an equal run of 64-token tiles out of
+//    the flattened list (sequence, key head, 16-head block, tile).  A run that
+//    covers a whole row of tiles writes its result; the others leave partial
+//    states (maximum, sum, output), which the join kernel folds in a fixed
+//    order: results are the same run to run.
+//  - Each warp streams its own 16 tokens of every tile through its own ring of
+//    shared memory (cp.async, no barrier between warps) and keeps its own
+//    online softmax state; the four warps are folded at the end of a run.
+//  - The query heads of a key head's group are the 16 rows of an m16n8k16
+//    product (padded rows cost tensor time that a memory-bound kernel has to
+//    spare); the probabilities' accumulator layout is the second product's
+//    operand layout, so they never leave registers.
+#pragma once
+
+#include <type_traits>
+
+#include <cuda_fp16.h>
+
+#include "sm100.cuh"
+
+namespace skl {
+
+struct PageView {                   // a paged tensor [pages, Hk, page, d], strides in elements, d contiguous
+    const void *ptr;
+    long long s_page, s_head, s_slot;
+};
+
+struct DecodeParams {
+    int B, H, Hk, G, nhb;           // nhb: blocks of 16 query heads per key head
+    int pages, page, max_pages;     // pages in the cache, slots in a page, columns of the table
+    int cap;                        // slots a sequence may have: min(max_pages * page, mass columns)
+    const void *q;                  // [B, H, d]
+    long long q_b, q_h;
+    PageView k, v;
+    const int *table, *len;
+    long long table_b;              // row stride of the table
+    float c;                        // scale * log2(e)
+    void *o;                        // [B, H, d] contiguous
+    float *lse;                     // [B, H]
+    float *part_o, *part_ml;        // [2 grid][16][d], [2 grid][16][2]
+    float *logits;                  // [B, H, cap] log2 units (mass wanted), or null
+    const float *mass;              // [B, Hk, mass_cap]
+    float *mass_out;
+    int mass_cap;
+    int grid;                       // CTAs of the split kernel
+    uint32_t *word;
+};
+
+constexpr int kDecTile = 64, kDecWarps = 4;
+
+template <int D>
+struct DecCfg {
+    static constexpr int ROW = D * 2;
+    static constexpr int STAGE = 16 * ROW * 2;                      // K and V rows of 16 tokens
+    static constexpr int NSTAGE = D == 128 ? 3 : 6;
+    static constexpr int RING = kDecWarps * NSTAGE * STAGE;
+    static constexpr int MERGE = kDecWarps * 16 * (D + 2) * 4;      // the warps' states, after the ring is drained
+    static constexpr int SMEM = RING > MERGE ? RING : MERGE;
+};
+
+// Weights are rounded to 16 bits for their product with V.  bf16 has fp32's
+// range; fp16 loses bits below 2^-14, so its weights are scaled to at most
+// 2^15 (the scale cancels against the sum): full precision down to 2^-29 of
+// the largest.
+template <typename T>
+constexpr float kWeightLog2 = std::is_same<T, __half>::value ? 15.f : 0.f;
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack16<__nv_bfloat16>(float lo, float hi) { return pack_bf16(lo, hi); }
+template <>
+__device__ __forceinline__ uint32_t pack16<__half>(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// D += A B, 16 x 8 x 16, fp32 accumulation.
+template <typename T>
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (std::is_same<T, __half>::value)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                     "{%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                     "{%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <bool TRANS>
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    if constexpr (TRANS)
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+    else
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+
+// 16 bytes to shared memory, zeros where `bytes` is 0 (nothing is read then).
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Slots of sequence b: its length clamped to [0, cap] (reported if outside).
+__device__ __forceinline__ int cache_len(const int *len, int b, int cap, uint32_t *word, bool report) {
+    const int n = __ldg(len + b);
+    if (report && (n < 0 || n > cap) && word) atomicOr(word, (uint32_t)kStatusBadLength);
+    return n < 0 ? 0 : (n > cap ? cap : n);
+}
+
+// Tiles of sequence b over its key heads and head blocks.
+__device__ __forceinline__ long long seq_tiles(int n, const DecodeParams &p) {
+    return (long long)((n + kDecTile - 1) / kDecTile) * p.Hk * p.nhb;
+}
+
+// The whole of the flattened list, and the run length of every CTA.
+struct TileMap {
+    long long total, chunk;
+};
+
+// Sums of a block of W warps: `mine` over all threads.
+template <int W>
+__device__ __forceinline__ long long block_sum(long long mine, long long *sh) {
+    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = mine;
+    __syncthreads();
+    mine = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) mine += sh[w];
+    __syncthreads();
+    return mine;
+}
+
+// All threads of the block call it.  `base` (if not null) gets the number of
+// tiles before sequence `upto`.
+template <int W>
+__device__ __forceinline__ TileMap tile_map(const DecodeParams &p, int upto, long long *base, long long *sh) {
+    long long mine = 0, before = 0;
+    for (int b = threadIdx.x; b < p.B; b += 32 * W) {
+        const long long t = seq_tiles(cache_len(p.len, b, p.cap, p.word, blockIdx.x == 0), p);
+        mine += t;
+        if (b < upto) before += t;
+    }
+    TileMap m;
+    m.total = block_sum<W>(mine, sh);
+    if (base) *base = block_sum<W>(before, sh);
+    m.chunk = m.total > 0 ? (m.total + p.grid - 1) / p.grid : 1;
+    return m;
+}
+
+// The sequence that holds tile u (u < total), and the tiles before it: blocks
+// of 32 W sequences at a time, a prefix sum within the block.
+template <int W>
+__device__ __forceinline__ int find_sequence(const DecodeParams &p, long long u, long long *base, long long *sh) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long done = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32 * W) {
+        const int b = b0 + (int)threadIdx.x;
+        const long long t = b < p.B ? seq_tiles(cache_len(p.len, b, p.cap, p.word, false), p) : 0;
+        long long v = t;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += y;
+        }
+        if (lane == 31) sh[warp] = v;
+        if (threadIdx.x == 0) sh[W] = -1;
+        __syncthreads();
+        long long first = done + v - t;
+        for (int w = 0; w < warp; ++w) first += sh[w];
+        if (u >= first && u < first + t) {
+            sh[W] = b;
+            sh[W + 1] = first;
+        }
+        for (int w = 0; w < W; ++w) done += sh[w];
+        __syncthreads();
+        if (sh[W] >= 0) break;
+        __syncthreads();
+    }
+    *base = sh[W + 1];
+    const int b = (int)sh[W];
+    __syncthreads();
+    return b;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kDecWarps * 32, 2) streamkl_decode_kernel(const DecodeParams p) {
+    using C = DecCfg<D>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ long long sh[kDecWarps + 2];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g4 = lane >> 2, c4 = lane & 3;                     // accumulator row and column pair
+
+    const TileMap tm = tile_map<kDecWarps>(p, 0, nullptr, sh);
+    long long u = (long long)blockIdx.x * tm.chunk;
+    const long long u_end = min(tm.total, u + tm.chunk), u_first = u;
+    if (u >= u_end) return;
+
+    long long base = 0;
+    int b = find_sequence<kDecWarps>(p, u, &base, sh);
+    int n = cache_len(p.len, b, p.cap, p.word, false);
+    while (u < u_end) {
+        const int nt = (n + kDecTile - 1) / kDecTile;
+        const int item = (int)((u - base) / nt);                 // (key head, head block)
+        const int hk = item / p.nhb, hb = item % p.nhb;
+        const int t0 = (int)((u - base) % nt);
+        const int t1 = (int)min((long long)nt, t0 + (u_end - u));
+        const int h0 = hk * p.G + hb * 16, nh = min(16, p.G - hb * 16);
+
+        // the group's query heads as the product's 16 rows (rows past nh are zero)
+        uint32_t qa[D / 16][4];
+        {
+            const T *q = static_cast<const T *>(p.q) + (size_t)b * p.q_b + (size_t)h0 * p.q_h;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int r = g4 + (x & 1) * 8, col = kk * 16 + c4 * 2 + (x >> 1) * 8;
+                    qa[kk][x] = r < nh ? __ldg(reinterpret_cast<const unsigned int *>(q + r * p.q_h + col)) : 0u;
+                }
+            }
+        }
+
+        // copies 16 tokens' K and V rows into a stage of this warp's ring; the
+        // 16-byte chunks of a row are permuted by the row so that eight rows of
+        // a column fall into different banks
+        const uint32_t ring = smem_u32(smem) + warp * C::NSTAGE * C::STAGE;
+        const T *kb = static_cast<const T *>(p.k.ptr) + hk * p.k.s_head;
+        const T *vb = static_cast<const T *>(p.v.ptr) + hk * p.v.s_head;
+        auto page_of = [&](int tile) -> int {                    // lane t < 16: page of this warp's token t, or -1
+            const int t = tile * kDecTile + warp * 16 + (lane & 15);
+            if (tile >= t1 || t >= n) return -1;
+            const int pg = __ldg(p.table + (size_t)b * p.table_b + t / p.page);
+            if ((unsigned)pg >= (unsigned)p.pages) {
+                if (p.word) atomicOr(p.word, (uint32_t)kStatusBadPage);
+                return -1;
+            }
+            return pg;
+        };
+        auto fetch = [&](int tile, int pg, int stage) {
+            constexpr int CH = D / 8;                            // 16-byte chunks in a row
+            constexpr int RPI = 32 / CH;                         // rows a warp copies at a time
+            const uint32_t dst = ring + stage * C::STAGE;
+#pragma unroll
+            for (int x = 0; x < 16 / RPI; ++x) {
+                const int r = x * RPI + lane / CH, ch = lane % CH;
+                const int row_pg = __shfl_sync(0xffffffffu, pg, r);
+                const int slot = (tile * kDecTile + warp * 16 + r) % p.page;
+                const bool ok = row_pg >= 0;
+                const size_t pgz = ok ? row_pg : 0, sl = ok ? slot : 0;
+                const uint32_t at = r * C::ROW + ((ch ^ (r & 7)) << 4);
+                cp_async16(dst + at, kb + pgz * p.k.s_page + sl * p.k.s_slot + ch * 8, ok ? 16 : 0);
+                cp_async16(dst + 16 * C::ROW + at, vb + pgz * p.v.s_page + sl * p.v.s_slot + ch * 8, ok ? 16 : 0);
+            }
+        };
+
+        float o[D / 8][4];
+#pragma unroll
+        for (int x = 0; x < D / 8; ++x) o[x][0] = o[x][1] = o[x][2] = o[x][3] = 0.f;
+        float M[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // rows g4 and g4 + 8
+
+        uint32_t seen[C::NSTAGE];                                // which of the stage's 16 tokens exist
+        int pg_next = page_of(t0);
+#pragma unroll
+        for (int s = 0; s < C::NSTAGE - 1; ++s) {
+            const int pg = pg_next;
+            pg_next = page_of(t0 + s + 1);
+            seen[s] = __ballot_sync(0xffffffffu, pg >= 0) & 0xffffu;
+            if (t0 + s < t1) fetch(t0 + s, pg, s);
+            cp_commit();
+        }
+        for (int tb = t0; tb < t1; tb += C::NSTAGE) {
+#pragma unroll
+            for (int s = 0; s < C::NSTAGE; ++s) {
+                const int tile = tb + s;
+                if (tile >= t1) break;
+                {   // the tile NSTAGE-1 ahead, into the stage that was read last
+                    constexpr int A = C::NSTAGE - 1;
+                    const int pg = pg_next, ns = (s + A) % C::NSTAGE;
+                    pg_next = page_of(tile + A + 1);
+                    seen[ns] = __ballot_sync(0xffffffffu, pg >= 0) & 0xffffu;
+                    if (tile + A < t1) fetch(tile + A, pg, ns);
+                    cp_commit();
+                }
+                cp_wait<C::NSTAGE - 1>();
+                __syncwarp();
+                const uint32_t kd = ring + s * C::STAGE, vd = kd + 16 * C::ROW;
+                // logits of 16 heads x 16 tokens
+                float y[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const int r = (lane & 7) + ((lane >> 4) << 3), ch = kk * 2 + ((lane >> 3) & 1);
+                    uint32_t kf[4];
+                    ldsm4<false>(kf, kd + r * C::ROW + ((ch ^ (r & 7)) << 4));
+                    mma_16816<T>(y[0], qa[kk], kf[0], kf[1]);
+                    mma_16816<T>(y[1], qa[kk], kf[2], kf[3]);
+                }
+                const uint32_t live = seen[s];
+                float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int tok = x * 8 + c4 * 2 + (e & 1);
+                        y[x][e] = (live >> tok) & 1 ? y[x][e] * p.c : -INFINITY;
+                        mx[e >> 1] = fmaxf(mx[e >> 1], y[x][e]);
+                    }
+                if (p.logits) {
+                    const int t = tile * kDecTile + warp * 16;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        if (g4 + e * 8 < nh) {
+                            float *dst = p.logits + ((size_t)b * p.H + h0 + g4 + e * 8) * p.cap + t;
+#pragma unroll
+                            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                                for (int z = 0; z < 2; ++z)
+                                    if (t + x * 8 + c4 * 2 + z < n) dst[x * 8 + c4 * 2 + z] = y[x][e * 2 + z];
+                        }
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
+                    mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
+                }
+                const bool up = mx[0] > M[0] || mx[1] > M[1];
+                if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float Mn = fmaxf(M[e], mx[e]);
+                        const float a = M[e] == -INFINITY ? 0.f : ex2(M[e] - Mn);
+                        l[e] *= a;
+#pragma unroll
+                        for (int x = 0; x < D / 8; ++x) { o[x][2 * e] *= a; o[x][2 * e + 1] *= a; }
+                        M[e] = Mn;
+                    }
+                }
+                uint32_t pa[4];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float base = (M[e] == -INFINITY ? 0.f : M[e]) - kWeightLog2<T>;
+                    const float p0 = ex2(y[0][2 * e] - base), p1 = ex2(y[0][2 * e + 1] - base);
+                    const float p2 = ex2(y[1][2 * e] - base), p3 = ex2(y[1][2 * e + 1] - base);
+                    l[e] += (p0 + p1) + (p2 + p3);
+                    pa[e] = pack16<T>(p0, p1);                   // rounded to the operand's 16 bits
+                    pa[e + 2] = pack16<T>(p2, p3);
+                }
+#pragma unroll
+                for (int dd = 0; dd < D / 16; ++dd) {
+                    const int r = (lane & 7) + (((lane >> 3) & 1) << 3), ch = dd * 2 + (lane >> 4);
+                    uint32_t vf[4];
+                    ldsm4<true>(vf, vd + r * C::ROW + ((ch ^ (r & 7)) << 4));
+                    mma_16816<T>(o[2 * dd], pa, vf[0], vf[1]);
+                    mma_16816<T>(o[2 * dd + 1], pa, vf[2], vf[3]);
+                }
+                __syncwarp();
+            }
+        }
+        cp_wait<0>();
+        __syncthreads();
+
+        // fold the four warps' states
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+            l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+        }
+        float *so = reinterpret_cast<float *>(smem), *sml = so + kDecWarps * 16 * D;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int r = warp * 16 + g4 + e * 8;
+#pragma unroll
+            for (int x = 0; x < D / 8; ++x)
+                *reinterpret_cast<float2 *>(so + r * D + x * 8 + c4 * 2) = make_float2(o[x][2 * e], o[x][2 * e + 1]);
+            if (c4 == 0) { sml[2 * r] = M[e] - kWeightLog2<T>; sml[2 * r + 1] = l[e]; }
+        }
+        __syncthreads();
+        const bool whole = t0 == 0 && t1 == nt;
+        const int slot = 2 * blockIdx.x + (u == u_first ? 0 : 1);
+        for (int x = threadIdx.x; x < nh * D; x += kDecWarps * 32) {
+            const int r = x / D, col = x % D;
+            float Mx = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kDecWarps; ++w) Mx = fmaxf(Mx, sml[2 * (w * 16 + r)]);
+            const float bs = Mx == -INFINITY ? 0.f : Mx;
+            float sum = 0.f, lsum = 0.f;
+#pragma unroll
+            for (int w = 0; w < kDecWarps; ++w) {
+                const float a = ex2(sml[2 * (w * 16 + r)] - bs);
+                sum = fmaf(a, so[(w * 16 + r) * D + col], sum);
+                lsum = fmaf(a, sml[2 * (w * 16 + r) + 1], lsum);
+            }
+            if (whole) {
+                const float ov = lsum == 0.f ? 0.f : sum / lsum;
+                static_cast<T *>(p.o)[((size_t)b * p.H + h0 + r) * D + col] = T(ov);
+                if (col == 0)
+                    p.lse[(size_t)b * p.H + h0 + r] =
+                        lsum == 0.f ? -INFINITY : 0.69314718055994530942f * (bs + lg2(lsum));
+            } else {
+                p.part_o[((size_t)slot * 16 + r) * D + col] = sum;
+                if (col == 0) {
+                    p.part_ml[((size_t)slot * 16 + r) * 2] = Mx;
+                    p.part_ml[((size_t)slot * 16 + r) * 2 + 1] = lsum;
+                }
+            }
+        }
+        __syncthreads();
+        u += t1 - t0;
+        if (u >= u_end) break;
+        while (u >= base + seq_tiles(n, p)) {                    // next sequence with tiles
+            base += seq_tiles(n, p);
+            ++b;
+            n = cache_len(p.len, b, p.cap, p.word, false);
+        }
+    }
+}
+
+// Folds the partial states of the rows that several CTAs shared, one CTA of D
+// threads a (sequence, query head); rows of empty sequences get 0 and -inf.
+template <typename T, int D>
+__global__ void __launch_bounds__(D) streamkl_decode_join_kernel(const DecodeParams p) {
+    __shared__ long long sh[D / 32];
+    const int b = blockIdx.x / p.H, h = blockIdx.x % p.H;
+    long long base;
+    const TileMap tm = tile_map<D / 32>(p, b, &base, sh);
+    const int n = cache_len(p.len, b, p.cap, p.word, false), nt = (n + kDecTile - 1) / kDecTile;
+    const size_t row = (size_t)b * p.H + h;
+    if (nt == 0) {
+        static_cast<T *>(p.o)[row * D + threadIdx.x] = T(0.f);
+        if (threadIdx.x == 0) p.lse[row] = -INFINITY;
+        return;
+    }
+    const int hk = h / p.G, hb = (h % p.G) / 16, r = (h % p.G) % 16;
+    const long long u0 = base + (long long)(hk * p.nhb + hb) * nt, u1 = u0 + nt;
+    const int c0 = (int)(u0 / tm.chunk), c1 = (int)((u1 - 1) / tm.chunk);
+    if (c0 == c1) return;                                        // one CTA had it whole
+    auto slot_of = [&](int c) { return 2 * c + ((long long)c * tm.chunk >= u0 ? 0 : 1); };
+    float M = -INFINITY;
+    for (int c = c0; c <= c1; ++c) M = fmaxf(M, p.part_ml[((size_t)slot_of(c) * 16 + r) * 2]);
+    const float bs = M == -INFINITY ? 0.f : M;
+    float sum = 0.f, l = 0.f;
+    for (int c = c0; c <= c1; ++c) {
+        const size_t s = (size_t)slot_of(c) * 16 + r;
+        const float a = ex2(p.part_ml[s * 2] - bs);
+        l = fmaf(a, p.part_ml[s * 2 + 1], l);
+        sum = fmaf(a, p.part_o[s * D + threadIdx.x], sum);
+    }
+    static_cast<T *>(p.o)[row * D + threadIdx.x] = T(l == 0.f ? 0.f : sum / l);
+    if (threadIdx.x == 0) p.lse[row] = l == 0.f ? -INFINITY : 0.69314718055994530942f * (bs + lg2(l));
+}
+
+// mass_out = mass + the weights of the new token, from the saved logits.
+__global__ void __launch_bounds__(256) streamkl_decode_mass_kernel(const DecodeParams p, int nx) {
+    const int bk = blockIdx.x / nx, x = blockIdx.x % nx, b = bk / p.Hk, hk = bk % p.Hk;
+    const int n = cache_len(p.len, b, p.cap, p.word, false);
+    for (int t = x * 256 + threadIdx.x; t < p.mass_cap; t += nx * 256) {
+        const size_t at = (size_t)bk * p.mass_cap + t;
+        if (t >= n) {
+            if (p.mass_out != p.mass) p.mass_out[at] = p.mass[at];
+            continue;
+        }
+        float w = 0.f;
+        for (int g = 0; g < p.G; ++g) {
+            const size_t row = (size_t)b * p.H + hk * p.G + g;
+            const float l2 = p.lse[row] * 1.4426950408889634074f;
+            w += l2 == -INFINITY ? 0.f : ex2(p.logits[row * p.cap + t] - l2);
+        }
+        p.mass_out[at] = p.mass[at] + w;
+    }
+}
+
+}  // namespace skl

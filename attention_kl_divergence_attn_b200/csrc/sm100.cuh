@@ -18,6 +18,8 @@ enum : uint32_t {
     kStatusTimeout = 1u << 0,   // some bounded wait gave up
     kStatusBadLength = 1u << 1, // a per-batch key length outside [0, N_K] (clamped)
     kStatusBounds = 1u << 2,    // bounds-checked build: an access outside its tensor (skipped)
+    kStatusBadPage = 1u << 3,   // a page table entry outside the cache (its tokens are skipped)
+    kStatusSharedPage = 1u << 4,// eviction from a page that several table entries name (left as it was)
     kStatusWhoShift = 8,        // bits 8..15: which wait (role-specific id)
     kStatusSiteShift = 16,      // bits 16..23: which checked access (bounds-checked build)
 };
@@ -441,6 +443,11 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, int a_mn, int b_
            | (1u << 10)                     // B format bf16
            | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16)
            | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// The same for fp16 operands (both of them; the formats are never mixed).
+__host__ __device__ constexpr uint32_t idesc_fp16(int M, int N, int a_mn, int b_mn) {
+    return idesc_bf16(M, N, a_mn, b_mn) & ~((1u << 7) | (1u << 10));
 }
 
 // ---------------------------------------------------------------- math

@@ -16,6 +16,9 @@
 #include "sm100.cuh"
 #include "fwd.cuh"
 #include "bwd.cuh"
+#include "mass.cuh"
+#include "decode.cuh"
+#include "evict.cuh"
 
 using namespace skl;
 
@@ -477,7 +480,7 @@ streamkl_status streamkl_selftest_timeout(void *workspace, size_t workspace_byte
     return cudaGetLastError() == cudaSuccess ? STREAMKL_OK : STREAMKL_ERR_CUDA;
 }
 
-int streamkl_version(void) { return 100; }
+int streamkl_version(void) { return 200; }
 
 size_t streamkl_workspace_size_ex(int B, int H, int H_kt, int H_ks, int N_Q, int N_K, int d_t, int d_s, int causal,
                                   int teacher_grads) {
@@ -533,7 +536,7 @@ streamkl_status streamkl_check(const void *workspace, void *stream, unsigned int
     if (cudaPeekAtLastError() != cudaSuccess) return STREAMKL_ERR_CUDA;
     if (word & kStatusTimeout) return STREAMKL_ERR_TIMEOUT;
     if (word & kStatusBounds) return STREAMKL_ERR_BOUNDS;
-    return (word & kStatusBadLength) ? STREAMKL_ERR_INVALID_ARG : STREAMKL_OK;
+    return (word & (kStatusBadLength | kStatusBadPage | kStatusSharedPage)) ? STREAMKL_ERR_INVALID_ARG : STREAMKL_OK;
 }
 
 streamkl_status streamkl_fwd(const void *q_t, const void *k_t, const void *q_s, const void *k_s, int B, int H,
@@ -742,3 +745,5 @@ extern "C" streamkl_status streamkl_fwd_noalloc(const void *q_t, const void *k_t
     *status_out = word;
     return (word & kStatusTimeout) ? STREAMKL_ERR_TIMEOUT : STREAMKL_OK;
 }
+
+#include "cache_api.cuh"

@@ -174,13 +174,15 @@ streamkl_status streamkl_workspace_init(void *workspace, size_t workspace_bytes,
 /* Synchronises `stream` and returns STREAMKL_ERR_TIMEOUT if a kernel of an
  * earlier call on this workspace gave up on a bounded wait,
  * STREAMKL_ERR_INVALID_ARG if a kernel met a per-batch key length outside
- * [0, N_K] (streamkl_fwd_ex / streamkl_bwd_ex; the length was clamped),
+ * [0, N_K] (streamkl_fwd_ex / streamkl_bwd_ex; the length was clamped) or a
+ * bad length or page of a cache (streamkl_decode / streamkl_evict),
  * STREAMKL_ERR_BOUNDS if (in the bounds-checked build, libstreamkl_checked.so)
  * a kernel found a TMA coordinate or global index outside its tensor and
  * skipped the access, STREAMKL_ERR_CUDA if the stream reports a CUDA error,
  * else STREAMKL_OK.  `code_out` (host pointer, nullable) receives the raw
  * device status word (0 = clean; bit 0 timeout, bit 1 bad length, bit 2
- * bounds, bits 8..15 which wait, bits 16..23 which checked access). */
+ * bounds, bit 3 bad page, bit 4 eviction from a shared page, bits 8..15 which
+ * wait, bits 16..23 which checked access). */
 streamkl_status streamkl_check(const void *workspace, void *stream, unsigned int *code_out);
 
 /*
@@ -279,6 +281,116 @@ streamkl_status streamkl_fwd_noalloc(const void *q_t, const void *k_t, const voi
                                      float scale_t, float scale_s, int causal,
                                      float *kl, float *lse_t, float *lse_s, float *loss_mean,
                                      void *stream, unsigned int *status_out);
+
+/*
+ * Serving with a bounded key-value cache.
+ * (Additions of this library; the paper has no counterpart.)
+ *
+ * What a distilled attention is served with: how much attention weight each
+ * key of a prompt has received (streamkl_key_mass, from the log-sum-exps that
+ * streamkl_fwd writes or its own), attention of one new token per sequence
+ * over a paged cache, which also adds the token's weights to the keys'
+ * accumulated ones (streamkl_decode), and eviction of the tokens with the
+ * smallest accumulated weight (streamkl_evict).
+ *
+ * Shared conventions, beyond those above:
+ *  - dtype: 0 = bf16, 1 = fp16, for all 16-bit tensors of a call.  d is 64 or
+ *    128 (else STREAMKL_ERR_UNSUPPORTED).  Lengths, weights and statistics are
+ *    int32 and fp32, 4-byte aligned; 16-bit tensors are 16-byte aligned.
+ *  - Query head h reads key head h / (H / H_k); H_k >= 1 divides H.
+ *  - *_stride: HOST pointer to the strides, in elements, of all dimensions but
+ *    the last, which is contiguous; NULL = dense in the order given.  A stride
+ *    must be positive and a multiple of 8 unless its dimension has one element.
+ *  - A paged cache is two tensors [num_pages, H_k, page_size, d] of any strides
+ *    (token-major pages are the same with other strides, and a contiguous cache
+ *    is one page a sequence).  Slot t of sequence b is slot t % page_size of
+ *    page page_table[b * table_stride + t / page_size].  A sequence has room
+ *    for cap = min(page_size * max_pages, 2^30) slots, or mass_cap if that is
+ *    less and weights are given.  Attention does not depend on the order of
+ *    the slots.
+ *  - seq_len, page_table are read on the device.  A length outside [0, cap] is
+ *    clamped; the tokens of a page outside [0, num_pages) are not attended to,
+ *    and a sequence that has one is not evicted from.  Either sets a bit that
+ *    streamkl_check() reports as STREAMKL_ERR_INVALID_ARG (status word bit 1:
+ *    length, bit 3: page, bit 4: see streamkl_evict).
+ *  - Only the first 256 bytes of `workspace` (the status word) are used.
+ *    `scratch` holds a call's intermediate results: calls that may overlap on
+ *    the GPU (two streams, two graphs) need one each.
+ */
+
+/* Bytes of scratch with which streamkl_key_mass runs fastest on the current
+ * device (0: none); with less it does not split long ranges over CTAs. */
+size_t streamkl_key_mass_scratch_size(int B, int H, int H_k, int N_Q, int N_K, int d, int lse_given);
+
+/*
+ * Accumulated attention weight of every key over N_Q query rows:
+ *   lse[b,h,i]    = log sum_j exp(scale <q[b,h,i], k[b,hk,j]>)   (visible j)
+ *   mass[b,hk,j] (+)= sum_{h of hk's group} sum_i exp(scale <q_i, k_j> - lse_i)
+ * q [B,H,N_Q,d] (q_stride: 3 values), k [B,H_k,N_K,d] (k_stride: 3 values),
+ * lse fp32 [B,H,N_Q], mass fp32 [B,H_k,N_K].  Visibility (causal, kv_len) is
+ * streamkl_fwd_ex's.
+ *  - lse_given = 1: lse is read (streamkl_fwd's lse_t or lse_s of the same
+ *    scale and mask, for instance); 0: it is computed and written.  A row whose
+ *    lse is -inf (no visible key) or +inf adds nothing.
+ *  - accumulate = 1 adds to mass (a prompt in several pieces), 0 overwrites it;
+ *    keys at and past kv_len[b] receive 0.
+ *  - Sums run in a fixed order: the same bits run to run.
+ * Keys are read at 2 d bytes; no N_Q x N_K buffer is written. */
+streamkl_status streamkl_key_mass(const void *q, const long long *q_stride, const void *k, const long long *k_stride,
+                                  int dtype, int B, int H, int H_k, int N_Q, int N_K, int d, float scale, int causal,
+                                  const int *kv_len, float *lse, int lse_given, float *mass, int accumulate,
+                                  void *workspace, size_t workspace_bytes, void *scratch, size_t scratch_bytes,
+                                  void *stream);
+
+/* Bytes of scratch that streamkl_decode requires on the current device. */
+size_t streamkl_decode_scratch_size(int B, int H, int H_k, int page_size, int max_pages, int d, int with_mass,
+                                    int mass_cap);
+
+/*
+ * Attention of one new token per sequence over a paged cache (whose last slot
+ * normally is that token's own key and value):
+ *   out[b,h] = sum_{t < seq_len[b]} w_t v_t,  w_t = exp(scale <q[b,h], k_t> - lse[b,h])
+ *   mass_out[b,hk,t] = mass[b,hk,t] + sum_{h of hk's group} w_t   (t < seq_len[b]; else mass)
+ * q [B,H,d] (q_stride: 2 values); k_pages, v_pages (3 values each); out
+ * [B,H,d] of q's type, dense; lse fp32 [B,H]; mass, mass_out fp32
+ * [B,H_k,mass_cap], both or neither NULL, equal (in place) or disjoint.
+ *  - seq_len[b] = 0 gives out = 0 and lse = -inf.
+ *  - Weights are rounded to 16 bits for their product with v only; their sums
+ *    and the statistics are fp32.  Results are the same bits run to run.
+ *  - Keys and values past a sequence's length are never read. */
+streamkl_status streamkl_decode(const void *q, const long long *q_stride, const void *k_pages,
+                                const long long *k_stride, const void *v_pages, const long long *v_stride, int dtype,
+                                int B, int H, int H_k, int d, int num_pages, int page_size, const int *page_table,
+                                int max_pages, long long table_stride, const int *seq_len, float scale, void *out,
+                                float *lse, const float *mass, float *mass_out, int mass_cap, void *workspace,
+                                size_t workspace_bytes, void *scratch, size_t scratch_bytes, void *stream);
+
+/* Bytes of scratch that streamkl_evict requires. */
+size_t streamkl_evict_scratch_size(int B, int H_k, int num_pages, int page_size, int max_pages, int mass_cap,
+                                   int budget);
+
+/*
+ * Evicts from every (sequence, key head) all but min(seq_len[b], budget)
+ * tokens.  Those stay whose rank (recent, weight, lowest slot) is highest:
+ * recent means pos >= next_pos[b] - recent (the newest tokens, which rank above
+ * every weight and alike); a weight that is negative or NaN ranks as 0.  Kept tokens below the new length stay in
+ * their slots; the others move, in order, into the slots that became free.
+ *   new_len[b]; mass_out, pos_out [B,H_k,mass_cap]: the kept tokens' values at
+ *   their new slots, 0 and -1 from new_len[b] on.
+ *  - k_pages, v_pages are changed in place (16-bit rows of any type); slots
+ *    from new_len[b] on keep what they held.
+ *  - pos int32 [B,H_k,mass_cap] (position of each slot's token) and next_pos
+ *    int32 [B] may be NULL when recent = 0; pos_out goes with pos.  Outputs
+ *    must not overlap inputs.  0 <= recent <= budget.
+ *  - A sequence that shares a page with another, or names one twice, while one
+ *    of the two evicts is left as it is (new_len = its length) and reported
+ *    (status word bit 4): moving rows would change the other's keys. */
+streamkl_status streamkl_evict(void *k_pages, const long long *k_stride, void *v_pages, const long long *v_stride,
+                               int B, int H_k, int d, int num_pages, int page_size, const int *page_table,
+                               int max_pages, long long table_stride, const int *seq_len, const float *mass,
+                               const int *pos, const int *next_pos, int mass_cap, int budget, int recent, int *new_len,
+                               float *mass_out, int *pos_out, void *workspace, size_t workspace_bytes, void *scratch,
+                               size_t scratch_bytes, void *stream);
 
 /*
  * Self-test of device failure reporting.  Launches one warp that waits, with
