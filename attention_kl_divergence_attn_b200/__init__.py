@@ -25,7 +25,6 @@ The autograd wrapper with temperature scaling is in ``.autograd``
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import functools
 import math
@@ -57,6 +56,8 @@ _F = ctypes.c_float
 def lib():
     """The loaded C library (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -381,82 +382,135 @@ def streamkl_loss_reduce(kl, factor, out=None, stream=None):
 
 
 # ---------------------------------------------------------------- cache operators
+# Serving calls take a few microseconds on the GPU, so what a call's shapes,
+# strides and types decide (the checks, the scratch size, the stride arrays) is
+# worked out once for each combination and looked up after that.
 _words: dict = {}
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _status_word(dev):
-    """The cache operators' status word on this device: 256 bytes that are never replaced, so that a
-    captured graph's pointer to them stays good."""
-    w = _words.get(dev.index)
+    """Address of the cache operators' status word on device index `dev`: 256 bytes that are never replaced,
+    so that a captured graph's pointer to them stays good."""
+    w = _words.get(dev)
     if w is None:
         if torch.cuda.is_current_stream_capturing():
             raise RuntimeError("the first cache operator on a device must run before a graph capture")
-        with torch.cuda.device(dev):
-            w = torch.zeros(_STATUS_BYTES, dtype=torch.uint8, device=dev)
-            torch.cuda.current_stream(dev).synchronize()       # cleared before any stream uses it
-        _words[dev.index] = w
-    return w
+        w = torch.zeros(_STATUS_BYTES, dtype=torch.uint8, device=torch.device("cuda", dev))
+        torch.cuda.current_stream(dev).synchronize()           # cleared before any stream uses it
+        _words[dev] = w
+    return w.data_ptr()
 
 
-@functools.lru_cache(maxsize=1024)
-def _scratch_bytes(fn, dev, *args):
-    return int(getattr(lib(), fn)(*args))
-
-
-@functools.lru_cache(maxsize=1024)
-def _strides(s):
-    return (ctypes.c_longlong * len(s))(*s)
+def _current_stream(dev):
+    return _raw_stream(dev) if _raw_stream else torch.cuda.current_stream(dev).cuda_stream
 
 
 def _on(dev, stream):
-    """Context that makes the call's device and stream current (nothing when they are already)."""
+    """Context that makes the call's device and stream current, or None when they are."""
     if stream is not None:
-        if stream.device != dev:
+        if stream.device.index != dev:
             raise ValueError("stream belongs to another device than the tensors")
         return torch.cuda.stream(stream)
-    if dev.index != torch.cuda.current_device():
-        return torch.cuda.device(dev)
-    return contextlib.nullcontext()
+    return None if dev == torch.cuda.current_device() else torch.cuda.device(dev)
 
 
-def _check_rows(name, t, ndim, like=None):
+def _sig(t):
+    """What the checks of a tensor depend on (None, and what is not a tensor, stand for themselves)."""
+    return (t.dtype, t.get_device(), t.shape, t.stride()) if isinstance(t, torch.Tensor) else t
+
+
+class _Meta:
+    """A signature with a tensor's attributes, for the checks."""
+
+    def __init__(self, sig):
+        self.dtype, self.device, self.shape, self._stride = sig
+        self.numel = math.prod(self.shape)
+
+    def stride(self, i):
+        return self._stride[i]
+
+    def contiguous(self):
+        n = 1
+        for size, s in zip(reversed(self.shape), reversed(self._stride)):
+            if size > 1 and s != n:
+                return self.numel == 0
+            n *= size
+        return True
+
+
+def _meta(sig):
+    return _Meta(sig) if isinstance(sig, tuple) else None
+
+
+def _check_rows(name, sig, ndim, like=None):
     """A CUDA 16-bit tensor whose rows (last dimension) are contiguous and 16-byte aligned."""
-    if not isinstance(t, torch.Tensor) or t.dtype not in _DTYPES or not t.is_cuda:
+    t = _meta(sig)
+    if t is None or t.dtype not in _DTYPES or t.device < 0:
         raise TypeError(f"{name} must be a CUDA bf16 or fp16 tensor")
-    if t.dim() != ndim or (t.stride(-1) != 1 and t.numel() > 0):
+    if len(t.shape) != ndim or (t.stride(-1) != 1 and t.numel > 0):
         raise ValueError(f"{name} must have {ndim} dimensions, the last one contiguous")
-    if t.numel() > 0 and (t.data_ptr() % 16 or any(n > 1 and (s % 8 or s <= 0)
-                                                   for n, s in zip(t.shape[:-1], t.stride()))):
-        raise ValueError(f"{name} must have rows on 16-byte boundaries (strides in multiples of 8, not expanded)")
+    if t.numel > 0 and any(n > 1 and (s % 8 or s <= 0) for n, s in zip(t.shape[:-1], t._stride)):
+        raise ValueError(f"{name} must have strides in positive multiples of 8 (rows on 16-byte boundaries)")
     if like is not None and (t.dtype != like.dtype or t.device != like.device):
         raise ValueError(f"{name} must have the type and device of the other tensors")
+    return t
 
 
-def _check_vec(name, t, dtype, shape, dev):
-    if (not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != dev or t.shape != torch.Size(shape)
-            or not t.is_contiguous()):
+def _check_vec(name, sig, dtype, shape, dev):
+    t = _meta(sig)
+    if t is None or t.dtype != dtype or t.device != dev or t.shape != torch.Size(shape) or not t.contiguous():
         raise ValueError(f"{name} must be a contiguous {str(dtype)[6:]} tensor {list(shape)} on the inputs' device")
 
 
 def _check_pages(k_pages, v_pages, page_table, seq_len, like=None):
-    _check_rows("k_pages", k_pages, 4, like)
-    _check_rows("v_pages", v_pages, 4, k_pages)
-    if k_pages.shape != v_pages.shape:
+    k = _check_rows("k_pages", k_pages, 4, like)
+    v = _check_rows("v_pages", v_pages, 4, k)
+    if k.shape != v.shape:
         raise ValueError("k_pages and v_pages must have one shape [pages, H_k, page_size, d]")
-    if k_pages.shape[1] < 1 or k_pages.shape[2] < 1:
+    if k.shape[1] < 1 or k.shape[2] < 1:
         raise ValueError("k_pages must have a key head and a slot a page")
-    dev = k_pages.device
-    if (not isinstance(page_table, torch.Tensor) or page_table.dtype != torch.int32 or page_table.device != dev
-            or page_table.dim() != 2 or (page_table.shape[1] > 1 and page_table.stride(1) != 1)):
+    t = _meta(page_table)
+    if (t is None or t.dtype != torch.int32 or t.device != k.device or len(t.shape) != 2
+            or (t.shape[1] > 1 and t.stride(1) != 1)):
         raise ValueError("page_table must be an int32 tensor [B, max_pages] with contiguous rows on the inputs' device")
-    _check_vec("seq_len", seq_len, torch.int32, (page_table.shape[0],), dev)
-    return dev
+    _check_vec("seq_len", seq_len, torch.int32, (t.shape[0],), k.device)
+    return k, v, t
+
+
+def _longs(s):
+    return (ctypes.c_longlong * len(s))(*s)
 
 
 def _overlap(a, b):
     pa, pb = a.data_ptr(), b.data_ptr()
     return pa < pb + b.numel() * b.element_size() and pb < pa + a.numel() * a.element_size()
+
+
+@functools.lru_cache(maxsize=4096)
+def _key_mass_plan(q_sig, k_sig, lse_sig, len_sig, out_sig, accumulate):
+    q = _check_rows("q", q_sig, 4)
+    k = _check_rows("k", k_sig, 4, q)
+    B, H, N_Q, d = q.shape
+    H_k, N_K = k.shape[1], k.shape[2]
+    if k.shape != (B, H_k, N_K, d):
+        raise ValueError("inconsistent shapes of q and k")
+    if H_k < 1 or H % H_k:
+        raise ValueError("the key heads must divide the query heads")
+    if accumulate and out_sig is None:
+        raise ValueError("accumulate needs out, the sums to add to")
+    dev = q.device
+    if len_sig is not None:
+        _check_vec("kv_len", len_sig, torch.int32, (B,), dev)
+    if lse_sig is not None:
+        _check_vec("lse", lse_sig, torch.float32, (B, H, N_Q), dev)
+    if out_sig is not None:
+        _check_vec("out", out_sig, torch.float32, (B, H_k, N_K), dev)
+    given = int(lse_sig is not None)
+    nbytes = int(lib().streamkl_key_mass_scratch_size(B, H, H_k, N_Q, N_K, d, given))
+    return (dev, torch.device("cuda", dev), (B, H_k, N_K), (B, H, N_Q), nbytes, 1.0 / math.sqrt(max(d, 1)),
+            _longs(q._stride[:3]), _longs(k._stride[:3]), (_DTYPES[q.dtype], B, H, H_k, N_Q, N_K, d))
 
 
 def streamkl_key_mass(q, k, lse=None, scale=None, causal=False, *, kv_len=None, out=None, accumulate=False,
@@ -473,38 +527,55 @@ def streamkl_key_mass(q, k, lse=None, scale=None, causal=False, *, kv_len=None, 
     key adds nothing.  ``out`` supplies mass; with ``accumulate`` the call
     adds to it (the pieces of a long prompt).  Gradients do not flow.
     """
-    _check_rows("q", q, 4)
-    _check_rows("k", k, 4, q)
-    B, H, N_Q, d = q.shape
-    H_k, N_K = k.shape[1], k.shape[2]
-    if k.shape != (B, H_k, N_K, d):
-        raise ValueError("inconsistent shapes of q and k")
-    if H_k < 1 or H % H_k:
-        raise ValueError("the key heads must divide the query heads")
-    if accumulate and out is None:
-        raise ValueError("accumulate needs out, the sums to add to")
-    dev = q.device
-    kv_len = _check_lengths(kv_len, B, dev)
-    if lse is not None:
-        _check_vec("lse", lse, torch.float32, (B, H, N_Q), dev)
-    if out is not None:
-        _check_vec("out", out, torch.float32, (B, H_k, N_K), dev)
-    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    dev, device, mass_shape, row_shape, nbytes, default, qs, ks, sizes = _key_mass_plan(
+        _sig(q), _sig(k), _sig(lse), _sig(kv_len), _sig(out), bool(accumulate))
+    on = _on(dev, stream)
+    if on is not None:
+        with on:
+            return streamkl_key_mass(q, k, lse, scale, causal, kv_len=kv_len, out=out, accumulate=accumulate)
+    word = _status_word(dev)
+    mass = torch.empty(mass_shape, dtype=torch.float32, device=device) if out is None else out
     given = lse is not None
-    with _on(dev, stream):
-        word = _status_word(dev)
-        mass = torch.empty(B, H_k, N_K, dtype=torch.float32, device=dev) if out is None else out
-        if not given:
-            lse = torch.empty(B, H, N_Q, dtype=torch.float32, device=dev)
-        nbytes = _scratch_bytes("streamkl_key_mass_scratch_size", dev.index, B, H, H_k, N_Q, N_K, d, int(given))
-        scratch = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
-        rc = lib().streamkl_key_mass(_ptr(q), _strides(q.stride()[:3]), _ptr(k), _strides(k.stride()[:3]),
-                                     _DTYPES[q.dtype], B, H, H_k, N_Q, N_K, d, scale, int(bool(causal)),
-                                     _ptr(kv_len), _ptr(lse), int(given), _ptr(mass), int(bool(accumulate)),
-                                     _ptr(word), _STATUS_BYTES, _ptr(scratch), nbytes, _stream(None))
+    if not given:
+        lse = torch.empty(row_shape, dtype=torch.float32, device=device)
+    scratch = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+    rc = lib().streamkl_key_mass(q.data_ptr(), qs, k.data_ptr(), ks, *sizes, default if scale is None else scale,
+                                 1 if causal else 0, None if kv_len is None else kv_len.data_ptr(), lse.data_ptr(),
+                                 given, mass.data_ptr(), 1 if accumulate else 0, word, _STATUS_BYTES,
+                                 None if scratch is None else scratch.data_ptr(), nbytes, _current_stream(dev))
     if rc:
         raise StreamKLError("streamkl_key_mass", rc)
     return mass, lse
+
+
+@functools.lru_cache(maxsize=4096)
+def _decode_plan(q_sig, k_sig, v_sig, table_sig, len_sig, mass_sig, mass_out_sig, o_sig, lse_sig):
+    q = _check_rows("q", q_sig, 3)
+    k, v, table = _check_pages(k_sig, v_sig, table_sig, len_sig, q)
+    dev = q.device
+    B, H, d = q.shape
+    pages, H_k, page, dk = k.shape
+    if dk != d or table.shape[0] != B:
+        raise ValueError("inconsistent shapes of q, k_pages and page_table")
+    if H % H_k:
+        raise ValueError("the key heads must divide the query heads")
+    cap = 0
+    if mass_sig is not None:
+        m = _meta(mass_sig)
+        cap = m.shape[-1] if m is not None and len(m.shape) == 3 else 0
+        _check_vec("mass", mass_sig, torch.float32, (B, H_k, cap), dev)
+        if mass_out_sig is not None:
+            _check_vec("mass_out", mass_out_sig, torch.float32, (B, H_k, cap), dev)
+    elif mass_out_sig is not None:
+        raise ValueError("mass_out needs mass")
+    if o_sig is not None or lse_sig is not None:
+        _check_vec("out[0]", o_sig, q.dtype, (B, H, d), dev)
+        _check_vec("out[1]", lse_sig, torch.float32, (B, H), dev)
+    max_pages = table.shape[1]
+    nbytes = int(lib().streamkl_decode_scratch_size(B, H, H_k, page, max_pages, d, int(mass_sig is not None), cap))
+    return (dev, torch.device("cuda", dev), (B, H, d), (B, H), nbytes, 1.0 / math.sqrt(max(d, 1)),
+            _longs(q._stride[:2]), _longs(k._stride[:3]), _longs(v._stride[:3]),
+            (_DTYPES[q.dtype], B, H, H_k, d, pages, page), max_pages, table.stride(0), cap)
 
 
 def streamkl_decode(q, k_pages, v_pages, page_table, seq_len, scale=None, *, mass=None, mass_out=None, out=None,
@@ -522,49 +593,65 @@ def streamkl_decode(q, k_pages, v_pages, page_table, seq_len, scale=None, *, mas
     the (out, lse) buffers.  Bad lengths and pages are reported by
     ``streamkl_check``.  Gradients do not flow.
     """
-    _check_rows("q", q, 3)
-    dev = _check_pages(k_pages, v_pages, page_table, seq_len, q)
-    B, H, d = q.shape
-    pages, H_k, page, dk = k_pages.shape
-    if dk != d or page_table.shape[0] != B:
-        raise ValueError("inconsistent shapes of q, k_pages and page_table")
-    if H % H_k:
-        raise ValueError("the key heads must divide the query heads")
-    cap = 0
+    o, lse = (None, None) if out is None else out
+    dev, device, o_shape, row_shape, nbytes, default, qs, ks, vs, sizes, max_pages, table_stride, cap = _decode_plan(
+        _sig(q), _sig(k_pages), _sig(v_pages), _sig(page_table), _sig(seq_len), _sig(mass), _sig(mass_out), _sig(o),
+        _sig(lse))
+    on = _on(dev, stream)
+    if on is not None:
+        with on:
+            return streamkl_decode(q, k_pages, v_pages, page_table, seq_len, scale, mass=mass, mass_out=mass_out,
+                                   out=out)
+    mass_ptr = mass_out_ptr = None
     if mass is not None:
-        cap = mass.shape[-1] if isinstance(mass, torch.Tensor) and mass.dim() == 3 else -1
-        _check_vec("mass", mass, torch.float32, (B, H_k, max(cap, 0)), dev)
-        if mass_out is None:
-            mass_out = mass
-        _check_vec("mass_out", mass_out, torch.float32, (B, H_k, cap), dev)
-        if mass_out.data_ptr() != mass.data_ptr() and _overlap(mass, mass_out):
-            raise ValueError("mass and mass_out must be one tensor or not overlap")
-    elif mass_out is not None:
-        raise ValueError("mass_out needs mass")
-    if out is not None:
-        _check_vec("out[0]", out[0], q.dtype, (B, H, d), dev)
-        _check_vec("out[1]", out[1], torch.float32, (B, H), dev)
-    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    with _on(dev, stream):
-        word = _status_word(dev)
-        if out is None:
-            o = torch.empty(B, H, d, dtype=q.dtype, device=dev)
-            lse = torch.empty(B, H, dtype=torch.float32, device=dev)
-        else:
-            o, lse = out
-        max_pages = page_table.shape[1]
-        with_mass = int(mass is not None)
-        nbytes = _scratch_bytes("streamkl_decode_scratch_size", dev.index, B, H, H_k, page, max_pages, d, with_mass,
-                                cap)
-        scratch = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        rc = lib().streamkl_decode(_ptr(q), _strides(q.stride()[:2]), _ptr(k_pages), _strides(k_pages.stride()[:3]),
-                                   _ptr(v_pages), _strides(v_pages.stride()[:3]), _DTYPES[q.dtype], B, H, H_k, d,
-                                   pages, page, _ptr(page_table), max_pages, page_table.stride(0), _ptr(seq_len),
-                                   scale, _ptr(o), _ptr(lse), _ptr(mass), _ptr(mass_out), cap, _ptr(word),
-                                   _STATUS_BYTES, _ptr(scratch), nbytes, _stream(None))
+        mass_ptr = mass_out_ptr = mass.data_ptr()
+        if mass_out is not None:
+            mass_out_ptr = mass_out.data_ptr()
+            if mass_out_ptr != mass_ptr and _overlap(mass, mass_out):
+                raise ValueError("mass and mass_out must be one tensor or not overlap")
+    word = _status_word(dev)
+    if out is None:
+        o, lse = torch.empty_like(q, memory_format=torch.contiguous_format), torch.empty(row_shape, dtype=torch.float32,
+                                                                                        device=device)
+    scratch = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+    rc = lib().streamkl_decode(q.data_ptr(), qs, k_pages.data_ptr(), ks, v_pages.data_ptr(), vs, *sizes,
+                               page_table.data_ptr(), max_pages, table_stride, seq_len.data_ptr(),
+                               default if scale is None else scale, o.data_ptr(), lse.data_ptr(), mass_ptr,
+                               mass_out_ptr, cap, word, _STATUS_BYTES,
+                               None if scratch is None else scratch.data_ptr(), nbytes, _current_stream(dev))
     if rc:
         raise StreamKLError("streamkl_decode", rc)
     return o, lse
+
+
+@functools.lru_cache(maxsize=4096)
+def _evict_plan(k_sig, v_sig, table_sig, len_sig, mass_sig, pos_sig, next_sig, out_sigs, budget, recent):
+    k, v, table = _check_pages(k_sig, v_sig, table_sig, len_sig)
+    dev = k.device
+    pages, H_k, page, d = k.shape
+    B, max_pages = table.shape
+    if budget < 0 or recent < 0 or recent > budget:
+        raise ValueError("budget and recent must satisfy 0 <= recent <= budget")
+    budget, recent = min(budget, 0x7fffffff), min(recent, 0x7fffffff)
+    m = _meta(mass_sig)
+    cap = m.shape[-1] if m is not None and len(m.shape) == 3 else 0
+    _check_vec("mass", mass_sig, torch.float32, (B, H_k, cap), dev)
+    if pos_sig is not None:
+        _check_vec("pos", pos_sig, torch.int32, (B, H_k, cap), dev)
+    if next_sig is not None:
+        _check_vec("next_pos", next_sig, torch.int32, (B,), dev)
+    if recent > 0 and (pos_sig is None or next_sig is None):
+        raise ValueError("recent needs pos and next_pos")
+    if out_sigs is not None:
+        _check_vec("out[0]", out_sigs[0], torch.int32, (B,), dev)
+        _check_vec("out[1]", out_sigs[1], torch.float32, (B, H_k, cap), dev)
+        if (out_sigs[2] is None) != (pos_sig is None):
+            raise ValueError("out[2] goes with pos")
+        if pos_sig is not None:
+            _check_vec("out[2]", out_sigs[2], torch.int32, (B, H_k, cap), dev)
+    nbytes = int(lib().streamkl_evict_scratch_size(B, H_k, pages, page, max_pages, cap, budget))
+    return (dev, torch.device("cuda", dev), (B,), max(nbytes, 16), _longs(k._stride[:3]), _longs(v._stride[:3]),
+            (B, H_k, d, pages, page), max_pages, table.stride(0), (cap, budget, recent))
 
 
 def streamkl_evict(k_pages, v_pages, page_table, seq_len, mass, budget, *, recent=0, pos=None, next_pos=None,
@@ -582,48 +669,31 @@ def streamkl_evict(k_pages, v_pages, page_table, seq_len, mass, budget, *, recen
     is None if none is given.  A sequence that shares pages with another one
     is left as it is and reported by ``streamkl_check``.
     """
-    dev = _check_pages(k_pages, v_pages, page_table, seq_len)
-    pages, H_k, page, d = k_pages.shape
-    B, max_pages = page_table.shape
-    budget, recent = int(budget), int(recent)
-    if budget < 0 or recent < 0 or recent > budget:
-        raise ValueError("budget and recent must satisfy 0 <= recent <= budget")
-    budget, recent = min(budget, 0x7fffffff), min(recent, 0x7fffffff)
-    cap = mass.shape[-1] if isinstance(mass, torch.Tensor) and mass.dim() == 3 else 0
-    _check_vec("mass", mass, torch.float32, (B, H_k, cap), dev)
-    if pos is not None:
-        _check_vec("pos", pos, torch.int32, (B, H_k, cap), dev)
-    if next_pos is not None:
-        _check_vec("next_pos", next_pos, torch.int32, (B,), dev)
-    if recent > 0 and (pos is None or next_pos is None):
-        raise ValueError("recent needs pos and next_pos")
-    if k_pages.numel() and k_pages.data_ptr() == v_pages.data_ptr():
-        raise ValueError("k_pages and v_pages must be two tensors")
-    if out is not None:
-        _check_vec("out[0]", out[0], torch.int32, (B,), dev)
-        _check_vec("out[1]", out[1], torch.float32, (B, H_k, cap), dev)
-        if (out[2] is None) != (pos is None):
-            raise ValueError("out[2] goes with pos")
-        if pos is not None:
-            _check_vec("out[2]", out[2], torch.int32, (B, H_k, cap), dev)
+    dev, device, len_shape, nbytes, ks, vs, sizes, max_pages, table_stride, tail = _evict_plan(
+        _sig(k_pages), _sig(v_pages), _sig(page_table), _sig(seq_len), _sig(mass), _sig(pos), _sig(next_pos),
+        None if out is None else tuple(_sig(o) for o in out), int(budget), int(recent))
+    on = _on(dev, stream)
+    if on is not None:
+        with on:
+            return streamkl_evict(k_pages, v_pages, page_table, seq_len, mass, budget, recent=recent, pos=pos,
+                                  next_pos=next_pos, out=out)
+    word = _status_word(dev)
+    if out is None:
+        new_len = torch.empty(len_shape, dtype=torch.int32, device=device)
+        mass_out = torch.empty_like(mass)
+        pos_out = None if pos is None else torch.empty_like(pos)
+    else:
+        new_len, mass_out, pos_out = out
         ins = [t for t in (seq_len, mass, pos, next_pos, page_table) if t is not None]
         if any(_overlap(o, i) for o in out if o is not None for i in ins):
             raise ValueError("out must not overlap the inputs")
-    with _on(dev, stream):
-        word = _status_word(dev)
-        if out is None:
-            new_len = torch.empty(B, dtype=torch.int32, device=dev)
-            mass_out = torch.empty_like(mass)
-            pos_out = None if pos is None else torch.empty_like(pos)
-        else:
-            new_len, mass_out, pos_out = out
-        nbytes = _scratch_bytes("streamkl_evict_scratch_size", dev.index, B, H_k, pages, page, max_pages, cap, budget)
-        scratch = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
-        rc = lib().streamkl_evict(_ptr(k_pages), _strides(k_pages.stride()[:3]), _ptr(v_pages),
-                                  _strides(v_pages.stride()[:3]), B, H_k, d, pages, page, _ptr(page_table), max_pages,
-                                  page_table.stride(0), _ptr(seq_len), _ptr(mass), _ptr(pos), _ptr(next_pos), cap,
-                                  budget, recent, _ptr(new_len), _ptr(mass_out), _ptr(pos_out), _ptr(word),
-                                  _STATUS_BYTES, _ptr(scratch), scratch.numel(), _stream(None))
+    scratch = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    rc = lib().streamkl_evict(k_pages.data_ptr(), ks, v_pages.data_ptr(), vs, *sizes, page_table.data_ptr(),
+                              max_pages, table_stride, seq_len.data_ptr(), mass.data_ptr(),
+                              None if pos is None else pos.data_ptr(),
+                              None if next_pos is None else next_pos.data_ptr(), *tail, new_len.data_ptr(),
+                              mass_out.data_ptr(), None if pos_out is None else pos_out.data_ptr(), word,
+                              _STATUS_BYTES, scratch.data_ptr(), nbytes, _current_stream(dev))
     if rc:
         raise StreamKLError("streamkl_evict", rc)
     return new_len, mass_out, pos_out

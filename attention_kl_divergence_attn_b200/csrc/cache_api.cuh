@@ -124,38 +124,76 @@ int paged_cap(int page_size, int max_pages, const void *mass, int mass_cap) {
     return (int)cap;
 }
 
+// Launch with the attributes of a dependent kernel (it may start while its
+// predecessor runs and calls grid_wait) and of a cluster, where asked for.
+template <typename K, typename... A>
+streamkl_status launch_ex(K kern, long long grid, int threads, int smem, cudaStream_t s, bool dependent, int cluster,
+                          A... args) {
+    cudaLaunchConfig_t c;
+    memset(&c, 0, sizeof c);
+    c.gridDim = dim3((unsigned)grid);
+    c.blockDim = dim3((unsigned)threads);
+    c.dynamicSmemBytes = (size_t)smem;
+    c.stream = s;
+    cudaLaunchAttribute at[2];
+    if (dependent) {
+        at[c.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[c.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (cluster > 1) {
+        at[c.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        at[c.numAttrs].val.clusterDim.x = (unsigned)cluster;
+        at[c.numAttrs].val.clusterDim.y = 1;
+        at[c.numAttrs++].val.clusterDim.z = 1;
+    }
+    c.attrs = at;
+    return cudaLaunchKernelEx(&c, kern, args...) == cudaSuccess ? STREAMKL_OK : STREAMKL_ERR_CUDA;
+}
+
 struct DecodeScratch {
     int grid;
+    bool by_row;
     size_t o, ml, logits, total;     // byte offsets and the whole
 };
+
+// Sequences of at most this many slots are not split: a CTA streams a whole
+// row, and there is no second kernel.
+constexpr int kByRowCap = 512;
 
 DecodeScratch decode_scratch(int B, int H, int H_k, int page_size, int max_pages, int d, bool with_mass, int mass_cap) {
     DecodeScratch r;
     const int G = H_k > 0 ? H / H_k : 0, nhb = (G + 15) / 16;
     const int cap = paged_cap(page_size, max_pages, with_mass ? &r : nullptr, mass_cap);
-    const long long tiles = (long long)B * H_k * nhb * (((long long)cap + kDecTile - 1) / kDecTile);
-    r.grid = (int)std::max<long long>(1, std::min<long long>(2ll * std::max(1, sm_count()), tiles));
+    const long long rows = (long long)B * H_k * nhb, tiles = rows * (((long long)cap + kDecTile - 1) / kDecTile);
+    r.by_row = cap <= kByRowCap;
+    r.grid = (int)(r.by_row ? rows : std::max<long long>(1, std::min<long long>(2ll * std::max(1, sm_count()), tiles)));
+    const size_t parts = r.by_row ? 0 : (size_t)r.grid * 2 * 16;
     r.o = 0;
-    r.ml = r.o + (size_t)r.grid * 2 * 16 * d * sizeof(float);
-    r.logits = r.ml + (size_t)r.grid * 2 * 16 * 2 * sizeof(float);
+    r.ml = r.o + parts * d * sizeof(float);
+    r.logits = r.ml + parts * 2 * sizeof(float);
     r.total = r.logits + (with_mass ? (size_t)B * H * cap * sizeof(float) : 0);
     return r;
 }
 
+// The split kernel counts a call's tiles in 32 bits, the mass blocks of the
+// finish kernel are a grid.
+bool decode_units_ok(int B, int H, int H_k, int cap, int mass_cap) {
+    const long long rows = (long long)B * H_k * ((H / H_k + 15) / 16);
+    return rows * ((cap + kDecTile - 1) / kDecTile + 4ll) <= (1ll << 30) &&
+           rows * (mass_cap / kFinishTokens + 1ll) <= (1ll << 30);
+}
+
 template <typename T, int D>
 streamkl_status launch_decode(const DecodeParams &p, cudaStream_t s) {
-    auto kern = streamkl_decode_kernel<T, D>;
+    auto kern = p.by_row ? streamkl_decode_kernel<T, D, true> : streamkl_decode_kernel<T, D, false>;
     if (set_smem(kern, DecCfg<D>::SMEM) != cudaSuccess) return STREAMKL_ERR_CUDA;
-    kern<<<p.grid, kDecWarps * 32, DecCfg<D>::SMEM, s>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return STREAMKL_ERR_CUDA;
-    streamkl_decode_join_kernel<T, D><<<(unsigned)(p.B * p.H), D, 0, s>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return STREAMKL_ERR_CUDA;
-    if (p.logits) {
-        const int nx = std::max(1, std::min(64, (p.mass_cap + 255) / 256));
-        streamkl_decode_mass_kernel<<<(unsigned)((long long)nx * p.B * p.Hk), 256, 0, s>>>(p, nx);
-        if (cudaGetLastError() != cudaSuccess) return STREAMKL_ERR_CUDA;
-    }
-    return STREAMKL_OK;
+    streamkl_status st = launch_ex(kern, p.grid, kDecWarps * 32, DecCfg<D>::SMEM, s, false, 1, p);
+    const bool mass = p.logits && !(p.by_row && p.nhb == 1);
+    if (st != STREAMKL_OK || (p.by_row && !mass)) return st;
+    const long long n_join = p.by_row ? 0 : ((long long)p.B * p.H + 3) / 4;
+    const int nx = std::max(1, (p.mass_cap + kFinishTokens - 1) / kFinishTokens);
+    const long long n_mass = mass ? (long long)nx * p.B * p.Hk : 0;
+    return launch_ex(streamkl_decode_finish_kernel<T, D>, n_join + n_mass, 128, 0, s, true, 1, p, (int)n_join, nx);
 }
 
 struct EvictScratch {
@@ -171,7 +209,7 @@ EvictScratch evict_scratch(int B, int H_k, int num_pages, int page_size, int max
     r.refused = r.owner + (size_t)num_pages * sizeof(int);
     r.moves = r.refused + (size_t)B * sizeof(int);
     r.lists = r.moves + (size_t)B * H_k * sizeof(int);
-    r.total = r.lists + (size_t)B * H_k * 2 * r.list * sizeof(int);
+    r.total = r.lists + (size_t)B * H_k * 4 * r.list * sizeof(int);
     return r;
 }
 
@@ -258,7 +296,7 @@ streamkl_status streamkl_decode(const void *q, const long long *q_stride, const 
                                 float *lse, const float *mass, float *mass_out, int mass_cap, void *workspace,
                                 size_t workspace_bytes, void *scratch, size_t scratch_bytes, void *stream) {
     if (!paged_shape_ok(B, H, H_k, num_pages, page_size, max_pages, dtype)) return STREAMKL_ERR_INVALID_ARG;
-    if (!(scale > 0.f) || scale == INFINITY || mass_cap < 0) return STREAMKL_ERR_INVALID_ARG;
+    if (!(scale > 0.f) || scale == INFINITY || mass_cap < 0 || mass_cap > kMaxCap) return STREAMKL_ERR_INVALID_ARG;
     if (d != 64 && d != 128) return STREAMKL_ERR_UNSUPPORTED;
     if (!workspace || workspace_bytes < kWorkspaceBytes) return STREAMKL_ERR_WORKSPACE;
     if (!aligned16(workspace) || !aligned16(scratch)) return STREAMKL_ERR_INVALID_ARG;
@@ -267,8 +305,10 @@ streamkl_status streamkl_decode(const void *q, const long long *q_stride, const 
     if (!q || !seq_len || !out || !lse || !aligned16(q) || !aligned16(out)) return STREAMKL_ERR_INVALID_ARG;
     if (!aligned4(lse) || !aligned4(mass) || !aligned4(mass_out)) return STREAMKL_ERR_INVALID_ARG;
     if (!cache_pointers_ok(k_pages, v_pages, num_pages, page_table, max_pages, seq_len)) return STREAMKL_ERR_INVALID_ARG;
+    if (!decode_units_ok(B, H, H_k, paged_cap(page_size, max_pages, mass, mass_cap), mass ? mass_cap : 0))
+        return STREAMKL_ERR_INVALID_ARG;
     const DecodeScratch ds = decode_scratch(B, H, H_k, page_size, max_pages, d, mass != nullptr, mass_cap);
-    if (!scratch || scratch_bytes < ds.total) return STREAMKL_ERR_WORKSPACE;
+    if (ds.total > 0 && (!scratch || scratch_bytes < ds.total)) return STREAMKL_ERR_WORKSPACE;
     const long long qs[3] = {0, q_stride ? q_stride[0] : (long long)H * d, q_stride ? q_stride[1] : d};
     const long long cont[3] = {(long long)H_k * page_size * d, (long long)page_size * d, d};
     const long long *ks = k_stride ? k_stride : cont, *vs = v_stride ? v_stride : cont;
@@ -295,6 +335,8 @@ streamkl_status streamkl_decode(const void *q, const long long *q_stride, const 
     p.logits = mass ? reinterpret_cast<float *>(sc + ds.logits) : nullptr;
     p.mass = mass; p.mass_out = mass_out; p.mass_cap = mass_cap;
     p.grid = ds.grid;
+    p.by_row = ds.by_row;
+    p.row_cost = d == 64 ? 3 : 2;
     p.word = static_cast<uint32_t *>(workspace);
     cudaStream_t s = (cudaStream_t)stream;
     if (dtype == kDtypeBf16)
@@ -315,7 +357,7 @@ streamkl_status streamkl_evict(void *k_pages, const long long *k_stride, void *v
                                float *mass_out, int *pos_out, void *workspace, size_t workspace_bytes, void *scratch,
                                size_t scratch_bytes, void *stream) {
     if (!paged_shape_ok(B, H_k, H_k, num_pages, page_size, max_pages, kDtypeBf16)) return STREAMKL_ERR_INVALID_ARG;
-    if (mass_cap < 0 || budget < 0 || recent < 0 || recent > budget) return STREAMKL_ERR_INVALID_ARG;
+    if (mass_cap < 0 || mass_cap > kMaxCap || budget < 0 || recent < 0 || recent > budget) return STREAMKL_ERR_INVALID_ARG;
     if (d != 64 && d != 128) return STREAMKL_ERR_UNSUPPORTED;
     if (!workspace || workspace_bytes < kWorkspaceBytes) return STREAMKL_ERR_WORKSPACE;
     if (!aligned16(workspace) || !aligned16(scratch)) return STREAMKL_ERR_INVALID_ARG;
@@ -330,6 +372,8 @@ streamkl_status streamkl_evict(void *k_pages, const long long *k_stride, void *v
     if (num_pages > 0 && k_pages && k_pages == v_pages) return STREAMKL_ERR_INVALID_ARG;
     if (slots && (!mass || !mass_out || mass == mass_out || (pos && pos == pos_out))) return STREAMKL_ERR_INVALID_ARG;
     if (!cache_pointers_ok(k_pages, v_pages, num_pages, page_table, max_pages, seq_len)) return STREAMKL_ERR_INVALID_ARG;
+    if ((long long)B * max_pages > 0x7fffffffll || (long long)num_pages * page_size > 0xffffffffll)
+        return STREAMKL_ERR_INVALID_ARG;
     const EvictScratch es = evict_scratch(B, H_k, num_pages, page_size, max_pages, mass_cap, budget);
     if (!scratch || scratch_bytes < es.total) return STREAMKL_ERR_WORKSPACE;
     const long long cont[3] = {(long long)H_k * page_size * d, (long long)page_size * d, d};
@@ -359,16 +403,26 @@ streamkl_status streamkl_evict(void *k_pages, const long long *k_stride, void *v
     p.list = es.list;
     p.word = static_cast<uint32_t *>(workspace);
     cudaStream_t s = (cudaStream_t)stream;
-    if (cudaMemsetAsync(p.owner, 0xff, (size_t)(num_pages + B) * sizeof(int), s) != cudaSuccess) return STREAMKL_ERR_CUDA;
-    const int smem = std::min(p.cap, kEvictSmemKeys) * (int)sizeof(uint32_t);
-    if (set_smem(streamkl_evict_select_kernel, kEvictSmemKeys * (int)sizeof(uint32_t)) != cudaSuccess)
+    // CTAs of a cluster: twice as many as long as each keeps over 2048 slots and all run at once
+    const long long rows = (long long)B * H_k;
+    int cs = 1;
+    while (cs < kEvictMaxCluster && p.cap / cs > 2048 &&
+           (rows * cs <= sm_count() || p.cap / cs > kEvictMaxWords * 32))
+        cs *= 2;
+    p.words = ((p.cap + 31) / 32 + cs - 1) / cs;
+    if (p.words > kEvictMaxWords) return STREAMKL_ERR_UNSUPPORTED;
+    if (set_smem(streamkl_evict_select_kernel, std::max(evict_smem(kEvictKeyWords), evict_smem(kEvictMaxWords))) !=
+        cudaSuccess)
         return STREAMKL_ERR_CUDA;
-    streamkl_evict_select_kernel<<<(unsigned)(B * H_k), kEvictThreads, smem, s>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return STREAMKL_ERR_CUDA;
+    st = launch_ex(streamkl_evict_claim_kernel, B, 256, 0, s, false, 1, p);
+    if (st != STREAMKL_OK) return st;
+    st = launch_ex(streamkl_evict_select_kernel, rows * cs, kEvictThreads, evict_smem(p.words), s, true, cs, p, cs);
+    if (st != STREAMKL_OK) return st;
+    // blocks for one and a half times what runs at once (8 an SM): rows with nothing to move leave early
     const int per = 256 / (d / 4);
-    const int nx = std::max(1, std::min(32, (p.list + per - 1) / per));
-    streamkl_evict_move_kernel<<<(unsigned)((long long)nx * B * H_k), 256, 0, s>>>(p, nx);
-    return cudaGetLastError() == cudaSuccess ? STREAMKL_OK : STREAMKL_ERR_CUDA;
+    const long long room = (12ll * std::max(1, sm_count()) + rows - 1) / rows;
+    const int nx = (int)std::max(1ll, std::min<long long>(room, (p.list + per - 1) / per));
+    return launch_ex(streamkl_evict_move_kernel, nx * rows, 256, 0, s, true, 1, p, nx);
 }
 
 }  // extern "C"

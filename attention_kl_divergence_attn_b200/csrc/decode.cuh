@@ -14,8 +14,9 @@
 //    the grid is fixed and every CTA takes an equal run of 64-token tiles out of
 //    the flattened list (sequence, key head, 16-head block, tile).  A run that
 //    covers a whole row of tiles writes its result; the others leave partial
-//    states (maximum, sum, output), which the join kernel folds in a fixed
-//    order: results are the same run to run.
+//    states (maximum, sum, output), which the finish kernel folds in a fixed
+//    order: results are the same run to run.  Where the table has no room for
+//    long sequences, a CTA takes a whole row and there is nothing to fold.
 //  - Each warp streams its own 16 tokens of every tile through its own ring of
 //    shared memory (cp.async, no barrier between warps) and keeps its own
 //    online softmax state; the four warps are folded at the end of a run.
@@ -56,6 +57,8 @@ struct DecodeParams {
     float *mass_out;
     int mass_cap;
     int grid;                       // CTAs of the split kernel
+    int row_cost;                   // a row's start-up, in units of tiles
+    int by_row;                     // one CTA a row of tiles, no partial states
     uint32_t *word;
 };
 
@@ -129,105 +132,125 @@ __device__ __forceinline__ int cache_len(const int *len, int b, int cap, uint32_
     return n < 0 ? 0 : (n > cap ? cap : n);
 }
 
-// Tiles of sequence b over its key heads and head blocks.
-__device__ __forceinline__ long long seq_tiles(int n, const DecodeParams &p) {
-    return (long long)((n + kDecTile - 1) / kDecTile) * p.Hk * p.nhb;
+// The flattened list counts units: a row of tiles (sequence, key head, head
+// block) is p.row_cost units of start-up (page table, queries, first copies,
+// the fold at its end) and one unit a tile, so that a CTA with many short rows
+// gets no more time's worth than one with a piece of a long row.
+__device__ __forceinline__ int row_tiles(int n) { return (n + kDecTile - 1) / kDecTile; }
+__device__ __forceinline__ int seq_units(int n, const DecodeParams &p) {
+    return n > 0 ? (row_tiles(n) + p.row_cost) * p.Hk * p.nhb : 0;
+}
+__device__ __forceinline__ int run_length(int total, int grid) {
+    return total > 0 ? (total + grid - 1) / grid : 1;
 }
 
-// The whole of the flattened list, and the run length of every CTA.
-struct TileMap {
-    long long total, chunk;
+// Where a CTA of the split kernel starts: the sequence that holds its first
+// unit, and the units before it.
+struct RunStart {
+    int total, base;
+    int b, n;
 };
 
-// Sums of a block of W warps: `mine` over all threads.
+// All threads of a block of W warps call it: a prefix sum of the sequences'
+// units, 32 W sequences at a time (twice when there are more, first for the total).
 template <int W>
-__device__ __forceinline__ long long block_sum(long long mine, long long *sh) {
-    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = mine;
-    __syncthreads();
-    mine = 0;
-#pragma unroll
-    for (int w = 0; w < W; ++w) mine += sh[w];
-    __syncthreads();
-    return mine;
-}
-
-// All threads of the block call it.  `base` (if not null) gets the number of
-// tiles before sequence `upto`.
-template <int W>
-__device__ __forceinline__ TileMap tile_map(const DecodeParams &p, int upto, long long *base, long long *sh) {
-    long long mine = 0, before = 0;
-    for (int b = threadIdx.x; b < p.B; b += 32 * W) {
-        const long long t = seq_tiles(cache_len(p.len, b, p.cap, p.word, blockIdx.x == 0), p);
-        mine += t;
-        if (b < upto) before += t;
-    }
-    TileMap m;
-    m.total = block_sum<W>(mine, sh);
-    if (base) *base = block_sum<W>(before, sh);
-    m.chunk = m.total > 0 ? (m.total + p.grid - 1) / p.grid : 1;
-    return m;
-}
-
-// The sequence that holds tile u (u < total), and the tiles before it: blocks
-// of 32 W sequences at a time, a prefix sum within the block.
-template <int W>
-__device__ __forceinline__ int find_sequence(const DecodeParams &p, long long u, long long *base, long long *sh) {
+__device__ __forceinline__ RunStart run_start(const DecodeParams &p, int *sh) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    long long done = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 32 * W) {
-        const int b = b0 + (int)threadIdx.x;
-        const long long t = b < p.B ? seq_tiles(cache_len(p.len, b, p.cap, p.word, false), p) : 0;
-        long long v = t;
+    RunStart r;
+    r.total = 0;
+    r.base = 0;
+    r.b = -1;
+    const int rounds = (p.B + 32 * W - 1) / (32 * W);
+    for (int pass = rounds > 1 ? 0 : 1; pass < 2; ++pass) {
+        int done = 0;
+        for (int b0 = 0; b0 < p.B; b0 += 32 * W) {
+            const int b = b0 + (int)threadIdx.x;
+            const int n = b < p.B ? cache_len(p.len, b, p.cap, p.word, blockIdx.x == 0) : 0;
+            const int t = seq_units(n, p);
+            int v = t;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, v, o);
-            if (lane >= o) v += y;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += y;
+            }
+            if (lane == 31) sh[warp] = v;
+            if (threadIdx.x == 0) sh[W] = -1;
+            __syncthreads();
+            int first = done + v - t;
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                if (w < warp) first += sh[w];
+                done += sh[w];
+            }
+            if (rounds == 1) r.total = done;
+            if (pass == 1) {
+                const int u = (int)blockIdx.x * run_length(r.total, p.grid);
+                if (u >= first && u < first + t) {
+                    sh[W] = b;
+                    sh[W + 1] = first;
+                    sh[W + 2] = n;
+                }
+                __syncthreads();
+                if (sh[W] >= 0) {
+                    r.b = sh[W];
+                    r.base = sh[W + 1];
+                    r.n = sh[W + 2];
+                    break;
+                }
+            }
+            __syncthreads();
         }
-        if (lane == 31) sh[warp] = v;
-        if (threadIdx.x == 0) sh[W] = -1;
-        __syncthreads();
-        long long first = done + v - t;
-        for (int w = 0; w < warp; ++w) first += sh[w];
-        if (u >= first && u < first + t) {
-            sh[W] = b;
-            sh[W + 1] = first;
-        }
-        for (int w = 0; w < W; ++w) done += sh[w];
-        __syncthreads();
-        if (sh[W] >= 0) break;
-        __syncthreads();
+        if (pass == 0) r.total = done;
     }
-    *base = sh[W + 1];
-    const int b = (int)sh[W];
     __syncthreads();
-    return b;
+    return r;
 }
 
-template <typename T, int D>
+// ROW: a CTA a row of tiles; else equal runs of the flattened list.
+template <typename T, int D, bool ROW>
 __global__ void __launch_bounds__(kDecWarps * 32, 2) streamkl_decode_kernel(const DecodeParams p) {
     using C = DecCfg<D>;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ long long sh[kDecWarps + 2];
+    __shared__ int sh[kDecWarps + 3];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g4 = lane >> 2, c4 = lane & 3;                     // accumulator row and column pair
 
-    const TileMap tm = tile_map<kDecWarps>(p, 0, nullptr, sh);
-    long long u = (long long)blockIdx.x * tm.chunk;
-    const long long u_end = min(tm.total, u + tm.chunk), u_first = u;
-    if (u >= u_end) return;
-
-    long long base = 0;
-    int b = find_sequence<kDecWarps>(p, u, &base, sh);
-    int n = cache_len(p.len, b, p.cap, p.word, false);
+    grid_release();
+    int b, n;
+    int u = 0, u_end = 1, u_first = 0, base = 0;                 // units
+    if constexpr (ROW) {
+        b = (int)(blockIdx.x / (p.Hk * p.nhb));
+        n = cache_len(p.len, b, p.cap, p.word, blockIdx.x % (p.Hk * p.nhb) == 0);
+    } else {
+        const RunStart rs = run_start<kDecWarps>(p, sh);
+        const int chunk = run_length(rs.total, p.grid);
+        u = u_first = (int)blockIdx.x * chunk;
+        u_end = min(rs.total, u + chunk);
+        if (u >= u_end) return;
+        b = rs.b;
+        n = rs.n;
+        base = rs.base;
+    }
     while (u < u_end) {
-        const int nt = (n + kDecTile - 1) / kDecTile;
-        const int item = (int)((u - base) / nt);                 // (key head, head block)
+        const int nt = row_tiles(n);
+        int item, t0, t1;                                        // (key head, head block), tiles of it
+        int row_end;
+        if constexpr (ROW) {
+            item = (int)(blockIdx.x % (p.Hk * p.nhb));
+            t0 = 0;
+            t1 = nt;
+            row_end = u_end;
+        } else {
+            item = (u - base) / (nt + p.row_cost);
+            const int tiles_at = base + item * (nt + p.row_cost) + p.row_cost;
+            row_end = tiles_at + nt;
+            t0 = max(0, u - tiles_at);
+            t1 = min(nt, max(0, u_end - tiles_at));
+        }
         const int hk = item / p.nhb, hb = item % p.nhb;
-        const int t0 = (int)((u - base) % nt);
-        const int t1 = (int)min((long long)nt, t0 + (u_end - u));
         const int h0 = hk * p.G + hb * 16, nh = min(16, p.G - hb * 16);
 
+        if (ROW || t0 < t1) {                                    // (else the run ends inside the start-up)
         // the group's query heads as the product's 16 rows (rows past nh are zero)
         uint32_t qa[D / 16][4];
         {
@@ -425,68 +448,200 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) streamkl_decode_kernel(cons
                 }
             }
         }
+        // one CTA had the whole group: its weights, from the logits just written
+        if (ROW && p.logits && p.nhb == 1) {
+            float *l2 = so;                                      // (the fold is done)
+            __syncthreads();
+            if (threadIdx.x < nh) l2[threadIdx.x] = p.lse[(size_t)b * p.H + h0 + threadIdx.x] * 1.4426950408889634074f;
+            __syncthreads();
+            for (int t = threadIdx.x; t < p.mass_cap; t += kDecWarps * 32) {
+                const size_t at = ((size_t)b * p.Hk + hk) * p.mass_cap + t;
+                float w = 0.f;
+                if (t < n)
+                    for (int r = 0; r < nh; ++r)
+                        w += l2[r] == -INFINITY
+                                 ? 0.f
+                                 : ex2(p.logits[((size_t)b * p.H + h0 + r) * p.cap + t] - l2[r]);
+                if (t < n || p.mass_out != p.mass) p.mass_out[at] = t < n ? p.mass[at] + w : p.mass[at];
+            }
+        }
         __syncthreads();
-        u += t1 - t0;
-        if (u >= u_end) break;
-        while (u >= base + seq_tiles(n, p)) {                    // next sequence with tiles
-            base += seq_tiles(n, p);
-            ++b;
-            n = cache_len(p.len, b, p.cap, p.word, false);
+        }
+        u = row_end;
+        if constexpr (!ROW) {
+            if (u >= u_end) break;
+            while (u >= base + seq_units(n, p)) {                // next sequence with tiles
+                base += seq_units(n, p);
+                ++b;
+                n = cache_len(p.len, b, p.cap, p.word, false);
+            }
         }
     }
 }
 
-// Folds the partial states of the rows that several CTAs shared, one CTA of D
-// threads a (sequence, query head); rows of empty sequences get 0 and -inf.
+// The piece of a row's units that several CTAs may share: first and last CTA,
+// and where each left its partial state.
+struct RowPieces {
+    int start, chunk;            // first unit of the row (its start-up included)
+    int c0, c1;
+    __device__ __forceinline__ size_t slot(int c) const { return 2 * (size_t)c + (c * chunk >= start ? 0 : 1); }
+};
+
+// A warp's sums over the sequences: all units, and those before sequence `upto`.
+__device__ __forceinline__ void warp_units(const DecodeParams &p, int upto, int &total, int &before) {
+    total = before = 0;
+    for (int b = threadIdx.x & 31; b < p.B; b += 32) {
+        const int t = seq_units(cache_len(p.len, b, p.cap, p.word, false), p);
+        total += t;
+        if (b < upto) before += t;
+    }
+    total = __reduce_add_sync(0xffffffffu, total);
+    before = __reduce_add_sync(0xffffffffu, before);
+}
+
+__device__ __forceinline__ RowPieces row_pieces(const DecodeParams &p, int total, int before, int nt, int item) {
+    RowPieces r;
+    r.chunk = run_length(total, p.grid);
+    r.start = before + item * (nt + p.row_cost);
+    r.c0 = (r.start + p.row_cost) / r.chunk;
+    r.c1 = (r.start + p.row_cost + nt - 1) / r.chunk;
+    return r;
+}
+
+// Joint maximum and sum (log2 units) of head r of the pieces; a whole warp
+// calls it and every lane gets the same bits.
+__device__ __forceinline__ void join_ml(const DecodeParams &p, const RowPieces &rp, int r, float &M, float &l) {
+    const int lane = threadIdx.x & 31;
+    M = -INFINITY;
+    for (int c = rp.c0 + lane; c <= rp.c1; c += 32) M = fmaxf(M, p.part_ml[(rp.slot(c) * 16 + r) * 2]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float bs = M == -INFINITY ? 0.f : M;
+    l = 0.f;
+    for (int c = rp.c0 + lane; c <= rp.c1; c += 32) {
+        const float *ml = p.part_ml + (rp.slot(c) * 16 + r) * 2;
+        l = fmaf(ex2(ml[0] - bs), ml[1], l);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+}
+
+constexpr int kFinishTokens = 1024;     // tokens of a mass block
+
+// After the split kernel, `n_join` blocks fold the partial states of the rows
+// that several CTAs shared, a warp a (sequence, query head), in a fixed order
+// (rows of empty sequences get 0 and -inf); the others add the new token's
+// weights to the accumulated ones, from the saved logits.  The latter fold the
+// few maxima and sums they need themselves, so the two do not wait for each other.
 template <typename T, int D>
-__global__ void __launch_bounds__(D) streamkl_decode_join_kernel(const DecodeParams p) {
-    __shared__ long long sh[D / 32];
-    const int b = blockIdx.x / p.H, h = blockIdx.x % p.H;
-    long long base;
-    const TileMap tm = tile_map<D / 32>(p, b, &base, sh);
-    const int n = cache_len(p.len, b, p.cap, p.word, false), nt = (n + kDecTile - 1) / kDecTile;
-    const size_t row = (size_t)b * p.H + h;
-    if (nt == 0) {
-        static_cast<T *>(p.o)[row * D + threadIdx.x] = T(0.f);
-        if (threadIdx.x == 0) p.lse[row] = -INFINITY;
+__global__ void __launch_bounds__(128) streamkl_decode_finish_kernel(const DecodeParams p, int n_join, int nx) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if ((int)blockIdx.x < n_join) {
+        const long long row = (long long)blockIdx.x * 4 + warp;
+        const int b = (int)(row / p.H), h = (int)(row % p.H);
+        if (b >= p.B) {
+            grid_wait();
+            return;
+        }
+        int total, before;
+        warp_units(p, b, total, before);
+        const int n = cache_len(p.len, b, p.cap, p.word, false), nt = row_tiles(n);
+        const int hk = h / p.G, hb = (h % p.G) / 16, r = (h % p.G) % 16;
+        RowPieces rp = {0, 1, 0, 0};
+        if (nt > 0) rp = row_pieces(p, total, before, nt, hk * p.nhb + hb);
+        grid_wait();
+        constexpr int E = D / 32;
+        T *o = static_cast<T *>(p.o) + (size_t)row * D + lane * E;
+        if (nt == 0) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] = T(0.f);
+            if (lane == 0) p.lse[row] = -INFINITY;
+            return;
+        }
+        if (rp.c0 == rp.c1) return;                              // one CTA had it whole
+        float M, l;
+        join_ml(p, rp, r, M, l);
+        const float bs = M == -INFINITY ? 0.f : M;
+        float sum[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) sum[e] = 0.f;
+#pragma unroll 4
+        for (int c = rp.c0; c <= rp.c1; ++c) {
+            const size_t s = rp.slot(c) * 16 + r;
+            const float a = ex2(p.part_ml[s * 2] - bs);
+#pragma unroll
+            for (int e = 0; e < E; e += 2) {
+                const float2 v = *reinterpret_cast<const float2 *>(p.part_o + s * D + lane * E + e);
+                sum[e] = fmaf(a, v.x, sum[e]);
+                sum[e + 1] = fmaf(a, v.y, sum[e + 1]);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = T(l == 0.f ? 0.f : sum[e] / l);
+        if (lane == 0) p.lse[row] = l == 0.f ? -INFINITY : 0.69314718055994530942f * (bs + lg2(l));
         return;
     }
-    const int hk = h / p.G, hb = (h % p.G) / 16, r = (h % p.G) % 16;
-    const long long u0 = base + (long long)(hk * p.nhb + hb) * nt, u1 = u0 + nt;
-    const int c0 = (int)(u0 / tm.chunk), c1 = (int)((u1 - 1) / tm.chunk);
-    if (c0 == c1) return;                                        // one CTA had it whole
-    auto slot_of = [&](int c) { return 2 * c + ((long long)c * tm.chunk >= u0 ? 0 : 1); };
-    float M = -INFINITY;
-    for (int c = c0; c <= c1; ++c) M = fmaxf(M, p.part_ml[((size_t)slot_of(c) * 16 + r) * 2]);
-    const float bs = M == -INFINITY ? 0.f : M;
-    float sum = 0.f, l = 0.f;
-    for (int c = c0; c <= c1; ++c) {
-        const size_t s = (size_t)slot_of(c) * 16 + r;
-        const float a = ex2(p.part_ml[s * 2] - bs);
-        l = fmaf(a, p.part_ml[s * 2 + 1], l);
-        sum = fmaf(a, p.part_o[s * D + threadIdx.x], sum);
-    }
-    static_cast<T *>(p.o)[row * D + threadIdx.x] = T(l == 0.f ? 0.f : sum / l);
-    if (threadIdx.x == 0) p.lse[row] = l == 0.f ? -INFINITY : 0.69314718055994530942f * (bs + lg2(l));
-}
-
-// mass_out = mass + the weights of the new token, from the saved logits.
-__global__ void __launch_bounds__(256) streamkl_decode_mass_kernel(const DecodeParams p, int nx) {
-    const int bk = blockIdx.x / nx, x = blockIdx.x % nx, b = bk / p.Hk, hk = bk % p.Hk;
-    const int n = cache_len(p.len, b, p.cap, p.word, false);
-    for (int t = x * 256 + threadIdx.x; t < p.mass_cap; t += nx * 256) {
+    // weights: tokens [t0, t0 + kFinishTokens) of one (sequence, key head)
+    __shared__ float l2[32];
+    const int x = (int)blockIdx.x - n_join, bk = x / nx, b = bk / p.Hk, hk = bk % p.Hk;
+    const int t0 = (x % nx) * kFinishTokens, t1 = min(p.mass_cap, t0 + kFinishTokens);
+    const int n = cache_len(p.len, b, p.cap, p.word, false), nt = row_tiles(n);
+    int total = 0, before = 0;
+    if (t0 < n && !p.by_row) warp_units(p, b, total, before);
+    // the split kernel writes neither of the two, so what it does not change is copied now
+    constexpr int PER = kFinishTokens / 128;
+    float w[PER];
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        const int t = t0 + k * 128 + (int)threadIdx.x;
         const size_t at = (size_t)bk * p.mass_cap + t;
-        if (t >= n) {
-            if (p.mass_out != p.mass) p.mass_out[at] = p.mass[at];
-            continue;
+        w[k] = t < t1 && (t < n || p.mass_out != p.mass) ? p.mass[at] : 0.f;
+    }
+    if (p.mass_out != p.mass) {
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            const int t = t0 + k * 128 + (int)threadIdx.x;
+            if (t >= n && t < t1) p.mass_out[(size_t)bk * p.mass_cap + t] = w[k];
         }
-        float w = 0.f;
-        for (int g = 0; g < p.G; ++g) {
-            const size_t row = (size_t)b * p.H + hk * p.G + g;
-            const float l2 = p.lse[row] * 1.4426950408889634074f;
-            w += l2 == -INFINITY ? 0.f : ex2(p.logits[row * p.cap + t] - l2);
+    }
+    grid_wait();
+    if (t0 >= n) return;
+    float sum[PER];
+#pragma unroll
+    for (int k = 0; k < PER; ++k) sum[k] = 0.f;
+    for (int g0 = 0; g0 < p.G; g0 += 32) {                       // 32 heads of the group at a time
+        const int ng = min(32, p.G - g0);
+        for (int g = warp; g < ng; g += 4) {
+            const int hb = (g0 + g) / 16, r = (g0 + g) % 16;
+            RowPieces rp = {0, 1, 0, 0};
+            if (!p.by_row) rp = row_pieces(p, total, before, nt, hk * p.nhb + hb);
+            float v;
+            if (rp.c0 == rp.c1) {
+                v = p.lse[(size_t)b * p.H + hk * p.G + g0 + g] * 1.4426950408889634074f;
+            } else {
+                float M, l;
+                join_ml(p, rp, r, M, l);
+                v = l == 0.f ? -INFINITY : (M == -INFINITY ? 0.f : M) + lg2(l);
+            }
+            if (lane == 0) l2[g] = v;
         }
-        p.mass_out[at] = p.mass[at] + w;
+        __syncthreads();
+        for (int g = 0; g < ng; ++g) {
+            const float *y = p.logits + ((size_t)b * p.H + hk * p.G + g0 + g) * p.cap;
+            const float s = l2[g];
+            if (s == -INFINITY) continue;
+#pragma unroll
+            for (int k = 0; k < PER; ++k) {
+                const int t = t0 + k * 128 + (int)threadIdx.x;
+                if (t < n) sum[k] += ex2(y[t] - s);
+            }
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        const int t = t0 + k * 128 + (int)threadIdx.x;
+        if (t < n && t < t1) p.mass_out[(size_t)bk * p.mass_cap + t] = w[k] + sum[k];
     }
 }
 

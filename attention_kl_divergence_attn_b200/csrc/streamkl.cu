@@ -5,6 +5,7 @@
 #include <cstdio>
 #include <cstring>
 #include <algorithm>
+#include <atomic>
 #include <set>
 #include <utility>
 #include <mutex>
@@ -62,12 +63,27 @@ bool make_map(CUtensorMap *m, const void *ptr, int d, int N, int BH, int rows) {
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Compute-capability major and SM count of the current device, looked up once
+// a device.
+constexpr int kMaxDevices = 64;
+std::atomic<int> g_device[kMaxDevices];          // major << 16 | SMs, 0 = not looked up
+
+int device_info() {
+    int dev = 0, major = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if (dev < kMaxDevices && (sms = g_device[dev].load(std::memory_order_relaxed)) != 0) return sms;
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return 0;
+    const int info = major << 16 | sms;
+    if (dev < kMaxDevices) g_device[dev].store(info, std::memory_order_relaxed);
+    return info;
+}
+
 streamkl_status check_device() {
-    int dev = 0, major = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return STREAMKL_ERR_CUDA;
-    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess)
-        return STREAMKL_ERR_CUDA;
-    return major == 10 ? STREAMKL_OK : STREAMKL_ERR_UNSUPPORTED;
+    const int info = device_info();
+    if (info == 0) return STREAMKL_ERR_CUDA;
+    return info >> 16 == 10 ? STREAMKL_OK : STREAMKL_ERR_UNSUPPORTED;
 }
 
 streamkl_status check_shape(int B, int H, int N_Q, int N_K, int d_t, int d_s, int causal, float scale_t,
@@ -122,13 +138,7 @@ cudaError_t set_smem(K kernel, int bytes) {
 
 constexpr int kFwdWarpgroups = 4;
 
-int sm_count() {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return 0;
-    return n;
-}
+int sm_count() { return device_info() & 0xffff; }
 
 // Key splits for the kernels that own 128-row query tiles and walk 64-key
 // tiles (the forward and the query-owner backward).  With few query tiles

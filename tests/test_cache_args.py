@@ -74,7 +74,8 @@ def test_key_mass_refusals(L, kw, rc):
     (dict(maxp=-1), 1), (dict(pages=-1), 1), (dict(q=0), 1), (dict(v=0), 1), (dict(v=24), 1), (dict(len=0), 1),
     (dict(len=18), 1), (dict(table=0), 1), (dict(table=18), 1), (dict(out=0), 1), (dict(out=24), 1), (dict(lse=0), 1),
     (dict(lse=18), 1), (dict(mass=16), 1), (dict(mo=16), 1), (dict(mass=18, mo=32, cap=32), 1), (dict(cap=-1), 1),
-    (dict(sc=0), 5), (dict(scb=100), 5), (dict(sc=20), 1), (dict(ts=-1), 1), (dict(qs=strides(256, 60)), 1),
+    (dict(sc=0, maxp=99), 5), (dict(scb=100, maxp=99), 5), (dict(sc=20), 1), (dict(ts=-1), 1),
+    (dict(qs=strides(256, 60)), 1),
     (dict(ks=strides(2048, 1024, 0)), 1), (dict(vs=strides(2048, -1024, 64)), 1)])
 def test_decode_refusals(L, kw, rc):
     assert decode(L, **kw) == rc
