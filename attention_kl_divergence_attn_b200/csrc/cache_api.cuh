@@ -21,57 +21,34 @@ bool stride_ok(const long long *s, const long long *extent) {
     return true;
 }
 
-// 4-D map over rows of d elements in [n3][n2][n1][d] with strides (in
-// elements) s3, s2, s1: box of 64 columns x `rows` rows, 128-byte swizzle,
-// zeros outside, so ragged tiles read zeros.
-bool make_rows_map(CUtensorMap *m, const void *ptr, int d, int n1, int n2, int n3, long long s1, long long s2,
-                   long long s3, int rows) {
+// 5-D map over rows of d elements in [n3][n2][n1][d] with strides (in
+// elements) s[0], s[1], s[2], as [n3][d / 64][n2][n1][64]: box of `rows` rows x
+// `heads` x `blocks` of 64 columns, 128-byte swizzle, zeros outside, so ragged
+// tiles read zeros.
+bool make_rows_map(CUtensorMap *m, const void *ptr, int d, int n1, int n2, int n3, const long long *s, int rows,
+                   int heads, int blocks) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t any = (cuuint64_t)d * 2;        // stride of a dimension with one element
-    cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)n1, (cuuint64_t)n2, (cuuint64_t)n3};
-    cuuint64_t strides[3] = {n1 > 1 ? (cuuint64_t)s1 * 2 : any, n2 > 1 ? (cuuint64_t)s2 * 2 : any,
-                             n3 > 1 ? (cuuint64_t)s3 * 2 : any};
-    cuuint32_t box[4] = {64, (cuuint32_t)rows, 1, 1};
-    cuuint32_t estr[4] = {1, 1, 1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void *>(ptr), dims, strides, box, estr,
+    cuuint64_t dims[5] = {64, (cuuint64_t)n1, (cuuint64_t)n2, (cuuint64_t)(d / 64), (cuuint64_t)n3};
+    cuuint64_t strides[4] = {n1 > 1 ? (cuuint64_t)s[2] * 2 : any, n2 > 1 ? (cuuint64_t)s[1] * 2 : any, 128,
+                             n3 > 1 ? (cuuint64_t)s[0] * 2 : any};
+    cuuint32_t box[5] = {64, (cuuint32_t)rows, (cuuint32_t)heads, (cuuint32_t)blocks, 1};
+    cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 5, const_cast<void *>(ptr), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Pieces that a streamed range of at most `tiles` tiles is cut into when there
-// are `items` owned tiles for two CTAs an SM: as key_splits above.
-int stat_splits(long long items, long long tiles) {
-    const long long slots = 2ll * sm_count();
-    if (slots <= 0 || items == 0 || items >= 4 * slots) return 1;
-    const int smax = (int)std::min<long long>(kMaxSplits, tiles / kMinSplitTiles);
-    int best = 1;
-    double best_t = 1e300;
-    for (int S = 1; S <= std::max(1, smax); ++S) {
-        const double t = (double)((items * S + slots - 1) / slots) / S * (1.0 + 0.02 * (S - 1));
-        if (t < best_t * (1.0 - 1e-9)) { best = S; best_t = t; }
-    }
-    return best;
+// Query tiles of 128 rows: whole heads of up to 64 rows are packed.
+void stat_rows(StatParams *p) {
+    p->pack = p->N_Q <= 64 ? std::min(p->G, 128 / p->N_Q) : 0;
+    p->R = p->pack ? (p->G + p->pack - 1) / p->pack : (p->N_Q + 127) / 128;
 }
 
-struct StatPlan {
-    long long lse_items, mass_items;
-    int lse_splits, mass_splits;
-    size_t bytes;                    // scratch of the splits
-};
-
-StatPlan stat_plan(int B, int H, int Hk, int N_Q, int N_K, bool lse_given) {
-    StatPlan s;
-    const long long G = H / Hk;
-    s.lse_items = (long long)B * Hk * ((G * N_Q + 127) / 128);
-    s.mass_items = (long long)B * Hk * ((N_K + 127) / 128);
-    s.lse_splits = lse_given ? 1 : stat_splits(s.lse_items, (N_K + 63) / 64);
-    s.mass_splits = stat_splits(s.mass_items, G * ((N_Q + 63) / 64));
-    const size_t a = s.lse_splits > 1 ? (size_t)s.lse_splits * 2 * B * H * N_Q * sizeof(float) : 0;
-    const size_t b = s.mass_splits > 1 ? (size_t)s.mass_splits * B * Hk * N_K * sizeof(float) : 0;
-    s.bytes = std::max(a, b);
-    return s;
-}
+// Runs of a call, and scratch for every run's two partial items.
+int stat_grid() { return std::max(1, sm_count()); }
+size_t stat_bytes() { return (size_t)stat_grid() * 2 * 2 * 128 * sizeof(float); }
 
 bool stat_shape_ok(int B, int H, int H_k, int N_Q, int N_K, int d, int dtype, int causal) {
     if (B < 0 || H < 0 || N_Q < 0 || N_K < 0 || H_k < 1 || (H > 0 && H % H_k != 0)) return false;
@@ -80,48 +57,8 @@ bool stat_shape_ok(int B, int H, int H_k, int N_Q, int N_K, int d, int dtype, in
     if (!causal && N_K == 0 && N_Q > 0 && B > 0 && H > 0) return false;
     if (dtype != kDtypeBf16 && dtype != kDtypeFp16) return false;
     return (long long)B * H <= (1ll << 24) && (long long)B * H_k <= (1ll << 24) && N_Q <= (1 << 24) && N_K <= (1 << 24) &&
-           (long long)H * N_Q < (1ll << 31);
-}
-
-template <int D, int MODE>
-streamkl_status launch_stat(const CUtensorMap &map, StatParams p, long long items, float *part, size_t part_bytes,
-                            int splits, cudaStream_t s) {
-    const long long rows = MODE == kRowLse ? (long long)p.B * p.H * p.N_Q : (long long)p.B * p.Hk * p.N_K;
-    const size_t need = (size_t)splits * (MODE == kRowLse ? 2 : 1) * rows * sizeof(float);
-    p.splits = splits > 1 && part && part_bytes >= need ? splits : 1;
-    p.part = part;
-    if (items * p.splits > 0x7fffffffll) return STREAMKL_ERR_INVALID_ARG;
-    auto kern = streamkl_stat_kernel<D, MODE>;
-    if (set_smem(kern, StatCfg<D>::SMEM) != cudaSuccess) return STREAMKL_ERR_CUDA;
-    kern<<<(unsigned)(items * p.splits), StatCfg<D>::THREADS, StatCfg<D>::SMEM, s>>>(map, p);
-    if (cudaGetLastError() != cudaSuccess) return STREAMKL_ERR_CUDA;
-    if (p.splits > 1) {
-        const unsigned blocks = (unsigned)((rows + 255) / 256);
-        if (MODE == kRowLse)
-            streamkl_lse_merge_kernel<<<blocks, 256, 0, s>>>(p.part, p.splits, rows, p.lse);
-        else
-            streamkl_mass_sum_kernel<<<blocks, 256, 0, s>>>(p.part, p.splits, rows, p.accumulate, p.mass);
-        if (cudaGetLastError() != cudaSuccess) return STREAMKL_ERR_CUDA;
-    }
-    return STREAMKL_OK;
-}
-
-bool paged_shape_ok(int B, int H, int H_k, int num_pages, int page_size, int max_pages, int dtype) {
-    if (B < 0 || H < 0 || H_k < 1 || num_pages < 0 || page_size < 1 || max_pages < 0) return false;
-    if (H > 0 && H % H_k != 0) return false;
-    if (dtype != kDtypeBf16 && dtype != kDtypeFp16) return false;
-    return (long long)B * H <= (1ll << 24) && (long long)B * H_k <= (1ll << 24) && B < (1 << 24);
-}
-
-bool cache_pointers_ok(const void *k, const void *v, int num_pages, const int *table, int max_pages, const int *len) {
-    if (num_pages > 0 && max_pages > 0 && (!k || !v || !aligned16(k) || !aligned16(v))) return false;
-    return (max_pages == 0 || table) && aligned4(table) && aligned4(len);
-}
-
-int paged_cap(int page_size, int max_pages, const void *mass, int mass_cap) {
-    long long cap = std::min<long long>((long long)page_size * max_pages, kMaxCap);
-    if (mass) cap = std::min<long long>(cap, mass_cap);
-    return (int)cap;
+           (long long)H * N_Q < (1ll << 31) &&
+           (double)B * H * ((N_Q + 127) / 128) * ((N_K + 127) / 128) < 1e11;      // a run's tiles are counted in 32 bits
 }
 
 // Launch with the attributes of a dependent kernel (it may start while its
@@ -148,6 +85,45 @@ streamkl_status launch_ex(K kern, long long grid, int threads, int smem, cudaStr
     }
     c.attrs = at;
     return cudaLaunchKernelEx(&c, kern, args...) == cudaSuccess ? STREAMKL_OK : STREAMKL_ERR_CUDA;
+}
+
+template <int D, int MODE>
+streamkl_status launch_stat(const void *q, const long long *qs, const void *k, const long long *ks, StatParams p,
+                            bool dependent, cudaStream_t s) {
+    using C = StatCfg<D>;
+    stat_rows(&p);
+    p.halves = MODE == kKeyMass && (p.pack ? p.pack : 1) * p.N_Q <= 64 ? 1 : 2;
+    CUtensorMap mq, mk;
+    if (!make_rows_map(&mq, q, D, p.N_Q, p.H, p.B, qs, p.pack ? p.N_Q : 128, std::max(1, p.pack),
+                       p.pack ? 1 : D / 64) ||
+        !make_rows_map(&mk, k, D, p.N_K, p.Hk, p.B, ks, 128, 1, D / 64))
+        return STREAMKL_ERR_CUDA;
+    // (no more runs than tiles)
+    const double tiles = (double)p.B * p.Hk * (p.pack ? p.R : (double)p.G * p.R) * ((p.N_K + 127) / 128);
+    p.grid = (int)std::min<double>(stat_grid(), tiles);
+    auto kern = streamkl_stat_kernel<D, MODE>;
+    if (set_smem(kern, C::SMEM) != cudaSuccess) return STREAMKL_ERR_CUDA;
+    streamkl_status st = launch_ex(kern, p.grid, C::THREADS, C::SMEM, s, dependent, 1, mq, mk, p);
+    if (st != STREAMKL_OK || p.grid == 1) return st;
+    return launch_ex(streamkl_stat_finish_kernel<MODE>, p.grid - 1, 128, 0, s, true, 1, p);
+}
+
+bool paged_shape_ok(int B, int H, int H_k, int num_pages, int page_size, int max_pages, int dtype) {
+    if (B < 0 || H < 0 || H_k < 1 || num_pages < 0 || page_size < 1 || max_pages < 0) return false;
+    if (H > 0 && H % H_k != 0) return false;
+    if (dtype != kDtypeBf16 && dtype != kDtypeFp16) return false;
+    return (long long)B * H <= (1ll << 24) && (long long)B * H_k <= (1ll << 24) && B < (1 << 24);
+}
+
+bool cache_pointers_ok(const void *k, const void *v, int num_pages, const int *table, int max_pages, const int *len) {
+    if (num_pages > 0 && max_pages > 0 && (!k || !v || !aligned16(k) || !aligned16(v))) return false;
+    return (max_pages == 0 || table) && aligned4(table) && aligned4(len);
+}
+
+int paged_cap(int page_size, int max_pages, const void *mass, int mass_cap) {
+    long long cap = std::min<long long>((long long)page_size * max_pages, kMaxCap);
+    if (mass) cap = std::min<long long>(cap, mass_cap);
+    return (int)cap;
 }
 
 struct DecodeScratch {
@@ -219,8 +195,9 @@ extern "C" {
 
 size_t streamkl_key_mass_scratch_size(int B, int H, int H_k, int N_Q, int N_K, int d, int lse_given) {
     (void)d;
+    (void)lse_given;
     if (B <= 0 || H <= 0 || H_k < 1 || H % H_k != 0 || N_Q <= 0 || N_K <= 0) return 0;
-    return stat_plan(B, H, H_k, N_Q, N_K, lse_given != 0).bytes;
+    return stat_bytes();
 }
 
 streamkl_status streamkl_key_mass(const void *q, const long long *q_stride, const void *k, const long long *k_stride,
@@ -252,35 +229,26 @@ streamkl_status streamkl_key_mass(const void *q, const long long *q_stride, cons
                              k_stride ? k_stride[1] : (long long)N_K * d, k_stride ? k_stride[2] : d};
     const long long qe[3] = {B, H, N_Q}, ke[3] = {B, H_k, N_K};
     if (!stride_ok(qs, qe) || !stride_ok(ks, ke)) return STREAMKL_ERR_INVALID_ARG;
+    if (!scratch || scratch_bytes < stat_bytes()) return STREAMKL_ERR_WORKSPACE;
     streamkl_status st = check_device();
     if (st != STREAMKL_OK) return st;
 
-    CUtensorMap mq, mk;
-    if (!make_rows_map(&mq, q, d, N_Q, H, B, qs[2], qs[1], qs[0], 64) ||
-        !make_rows_map(&mk, k, d, N_K, H_k, B, ks[2], ks[1], ks[0], 64))
-        return STREAMKL_ERR_CUDA;
-    const StatPlan plan = stat_plan(B, H, H_k, N_Q, N_K, lse_given != 0);
     StatParams p;
     memset(&p, 0, sizeof p);
     p.B = B; p.H = H; p.Hk = H_k; p.G = H / H_k; p.N_Q = N_Q; p.N_K = N_K; p.causal = causal;
     p.kv_len = kv_len;
     p.c = scale * kLog2e;
-    p.idesc = dtype == kDtypeBf16 ? idesc_bf16(128, 64, 0, 0) : idesc_fp16(128, 64, 0, 0);
+    p.fp16 = dtype == kDtypeFp16;
     p.lse = lse; p.mass = mass; p.accumulate = accumulate;
+    p.part = static_cast<float *>(scratch);
     p.st.word = static_cast<uint32_t *>(workspace);
     p.st.budget_ns = kWaitBudgetNs;
-    float *part = static_cast<float *>(scratch);
     if (!lse_given) {
-        p.own = q; p.own_b = qs[0]; p.own_h = qs[1]; p.own_n = qs[2];
-        p.n_own = (int)(((long long)p.G * N_Q + 127) / 128);
-        st = d == 64 ? launch_stat<64, kRowLse>(mk, p, plan.lse_items, part, scratch_bytes, plan.lse_splits, s)
-                     : launch_stat<128, kRowLse>(mk, p, plan.lse_items, part, scratch_bytes, plan.lse_splits, s);
+        st = d == 64 ? launch_stat<64, kRowLse>(q, qs, k, ks, p, false, s) : launch_stat<128, kRowLse>(q, qs, k, ks, p, false, s);
         if (st != STREAMKL_OK) return st;
     }
-    p.own = k; p.own_b = ks[0]; p.own_h = ks[1]; p.own_n = ks[2];
-    p.n_own = (N_K + 127) / 128;
-    return d == 64 ? launch_stat<64, kKeyMass>(mq, p, plan.mass_items, part, scratch_bytes, plan.mass_splits, s)
-                   : launch_stat<128, kKeyMass>(mq, p, plan.mass_items, part, scratch_bytes, plan.mass_splits, s);
+    return d == 64 ? launch_stat<64, kKeyMass>(q, qs, k, ks, p, !lse_given, s)
+                   : launch_stat<128, kKeyMass>(q, qs, k, ks, p, !lse_given, s);
 }
 
 size_t streamkl_decode_scratch_size(int B, int H, int H_k, int page_size, int max_pages, int d, int with_mass,

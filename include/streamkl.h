@@ -318,8 +318,7 @@ streamkl_status streamkl_fwd_noalloc(const void *q_t, const void *k_t, const voi
  *    the GPU (two streams, two graphs) need one each.
  */
 
-/* Bytes of scratch with which streamkl_key_mass runs fastest on the current
- * device (0: none); with less it does not split long ranges over CTAs. */
+/* Bytes of scratch that streamkl_key_mass requires on the current device. */
 size_t streamkl_key_mass_scratch_size(int B, int H, int H_k, int N_Q, int N_K, int d, int lse_given);
 
 /*

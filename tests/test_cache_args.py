@@ -26,7 +26,7 @@ def strides(*s):
 
 def mass(L, **kw):
     a = dict(q=16, qs=None, k=16, ks=None, dtype=0, B=1, H=4, Hk=2, N_Q=8, N_K=9, d=64, scale=0.1, causal=0, kv=0,
-             lse=16, given=0, mass=16, acc=0, ws=16, wsb=256, sc=0, scb=0)
+             lse=16, given=0, mass=16, acc=0, ws=16, wsb=256, sc=16, scb=1 << 30)
     a.update(kw)
     return L.streamkl_key_mass(p(a["q"]), a["qs"], p(a["k"]), a["ks"], a["dtype"], a["B"], a["H"], a["Hk"], a["N_Q"],
                                a["N_K"], a["d"], a["scale"], a["causal"], p(a["kv"]), p(a["lse"]), a["given"],
@@ -63,7 +63,7 @@ COMMON = [(dict(ws=0), 5), (dict(wsb=255), 5), (dict(ws=20), 1), (dict(d=96), 2)
     (dict(H=3), 1), (dict(dtype=2), 1), (dict(causal=2), 1), (dict(causal=1, N_Q=10), 1), (dict(N_K=0), 1),
     (dict(scale=0.0), 1), (dict(scale=math.inf), 1), (dict(scale=math.nan), 1), (dict(lse=0), 1), (dict(mass=0), 1),
     (dict(mass=18), 1), (dict(lse=18), 1), (dict(kv=18), 1), (dict(given=2), 1), (dict(acc=2), 1), (dict(q=0), 1),
-    (dict(q=24), 1), (dict(sc=20), 1), (dict(N_Q=1 << 25), 1), (dict(qs=strides(4096, 512, 60)), 1),
+    (dict(q=24), 1), (dict(sc=20), 1), (dict(N_Q=1 << 25), 1), (dict(sc=0), 5), (dict(scb=100), 5), (dict(qs=strides(4096, 512, 60)), 1),
     (dict(ks=strides(1, 0, 64)), 1), (dict(ks=strides(1, 576, -64)), 1)])
 def test_key_mass_refusals(L, kw, rc):
     assert mass(L, **kw) == rc

@@ -43,6 +43,11 @@ MASS = [
     (1, 3, 3, 1500, 1501, 64, True, BF, None),
     (1, 1, 1, 3000, 40, 128, False, BF, None),
     (1, 4, 1, 63, 12000, 128, True, FP, None),
+    # many tiles a run
+    (2, 8, 2, 1700, 1750, 64, True, BF, None),
+    (2, 8, 4, 1500, 1601, 128, False, FP, (1601, 900)),
+    (2, 12, 3, 40, 30000, 128, True, FP, None),
+    (1, 9, 1, 17, 60000, 64, False, BF, (59990,)),
 ]
 
 
