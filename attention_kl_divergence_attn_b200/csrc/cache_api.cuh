@@ -48,7 +48,7 @@ void stat_rows(StatParams *p) {
 
 // Runs of a call, and scratch for every run's two partial items.
 int stat_grid() { return std::max(1, sm_count()); }
-size_t stat_bytes() { return (size_t)stat_grid() * 2 * 2 * 128 * sizeof(float); }
+size_t stat_bytes() { return (size_t)stat_grid() * 2 * 2 * 256 * sizeof(float); }
 
 bool stat_shape_ok(int B, int H, int H_k, int N_Q, int N_K, int d, int dtype, int causal) {
     if (B < 0 || H < 0 || N_Q < 0 || N_K < 0 || H_k < 1 || (H > 0 && H % H_k != 0)) return false;
@@ -105,7 +105,7 @@ streamkl_status launch_stat(const void *q, const long long *qs, const void *k, c
     if (set_smem(kern, C::SMEM) != cudaSuccess) return STREAMKL_ERR_CUDA;
     streamkl_status st = launch_ex(kern, p.grid, C::THREADS, C::SMEM, s, dependent, 1, mq, mk, p);
     if (st != STREAMKL_OK || p.grid == 1) return st;
-    return launch_ex(streamkl_stat_finish_kernel<MODE>, p.grid - 1, 128, 0, s, true, 1, p);
+    return launch_ex(streamkl_stat_finish_kernel<MODE>, p.grid - 1, 256, 0, s, true, 1, p);
 }
 
 bool paged_shape_ok(int B, int H, int H_k, int num_pages, int page_size, int max_pages, int dtype) {

@@ -3,35 +3,35 @@
 //     lse_i  = log sum_j exp(y_ij),   y_ij = scale q_i . k_j  (visible j)
 //     mass_j = sum_{heads of the group} sum_i exp(y_ij - lse_i)
 // without writing the matrix.  Both sums run in one kernel template:
-//   MODE = kRowLse: an item is 128 query rows, the keys are streamed.
-//   MODE = kKeyMass: an item is 128 keys of one key head, the query rows of all
+//   MODE = kRowLse: an item is 256 query rows, the keys are streamed.
+//   MODE = kKeyMass: an item is 256 keys of one key head, the query rows of all
 //          heads of its group are streamed.
-// The item's rows are the MMA's M dimension (tensor-memory lanes), the streamed
-// ones its N dimension, so in both modes a thread reads one owned row of a
-// logit tile and its sum over the streamed rows stays in the thread.  Up to 64
-// query rows a head are packed: a tile holds as many whole heads as fit.
+// The item's rows are the MMA's M dimension (tensor-memory lanes, two MMAs a
+// streamed tile), the streamed ones its N dimension, so in both modes a thread
+// reads one owned row of a logit tile and its sum over the streamed rows stays
+// in the thread.  Up to 64 query rows a head are packed: a tile of 128 rows holds
+// as many whole heads as fit.
 //
 // One CTA an SM.  The tiles of all items are one list, of which every CTA takes
 // an equal run, so that causal, padded and few-item problems balance alike; an
 // item that two runs share leaves partial sums, which the finish kernel adds in
 // a fixed order (the same bits run to run).
-//   warp 0      producer: TMA loads of an item's rows (two buffers) and of the
-//               streamed tiles (a ring).
-//   warps 1, 2  MMA issuers, one a half of the streamed tiles.  Warp 1 owns the
-//               tensor memory: six 128 x 64 logit tiles of fp32 (halves), and the
-//               item's rows (two buffers, packed 16-bit) as the A operand, so that
-//               a tcgen05.mma reads only the streamed tile from shared memory (with
-//               A in shared memory too, a tile took 870 clocks of its bandwidth
-//               instead of 512).
-//   warps 3..18 four warpgroups taking the halves in turn; thread = owned row.
-//   warps 19..22 copy an item's rows from shared to tensor memory, an item ahead,
-//               and in kKeyMass write the -lse * log2(e) of a half's rows as a table
-//               for one warpgroup each (when every warp of the warpgroups did that
-//               for itself, two thirds of the issued instructions were not sums).
+//   warp 0      producer: TMA loads of an item's rows and of the streamed tiles
+//               (128 rows, a ring).
+//   warps 1, 2  MMA issuers, one a half (64 rows) of the streamed tiles.  Warp 1
+//               owns the tensor memory: four 128 x 64 logit tiles of fp32 (item
+//               half, tile half), and the item's rows (two buffers, packed 16-bit)
+//               as the A operand, so that a tcgen05.mma reads only the streamed
+//               tile from shared memory (with A in shared memory too, 128 x 128
+//               logits took 870 clocks of its bandwidth instead of 512).
+//   warps 3..18 four warpgroups, one a logit tile; thread = owned row.
+//   warps 19..22 copy an item's rows from shared to tensor memory, an item ahead;
+//               in kKeyMass two of them write the -lse * log2(e) of a half's rows
+//               as a table for the warpgroups.
 //   warp 23     adds the warpgroups' sums of an item and writes it.
-// Work bound: one exponential a pair (16 a clock and SM: 1024 clocks a tile)
-// against 2 d flops (512 clocks a tile at d = 128).  One thread takes some 400
-// clocks of its own for a half's waits, MMAs and commits, hence two issuers.
+// Work bound: one exponential a pair (16 a clock and SM: 2048 clocks a tile)
+// against 2 d flops (1024 clocks a tile at d = 128) and 32 KB of streamed rows
+// from L2 (items of 128 rows read them twice as often, 9 TB/s over all SMs).
 #pragma once
 
 #include "sm100.cuh"
@@ -52,60 +52,57 @@ struct StatParams {
     float *lse;                  // [B, H, N_Q]: written (kRowLse) or read (kKeyMass)
     float *mass;                 // [B, Hk, N_K]
     int accumulate;              // add to mass instead of overwriting it
-    float *part;                 // [grid][2][128][2]: partial sums of a run's first and last item
+    float *part;                 // [grid][2][2][256]: partial sums of a run's first and last item
     int grid;                    // runs
     DevStatus st;
 };
 
 template <int D>
 struct StatCfg {
-    static constexpr int BM = 128, BN = 128;
+    static constexpr int BM = 256, BN = 128;                  // rows of an item, of a streamed tile
     static constexpr int BOX = 128 * 128;                     // [128 rows][64 columns] 16-bit
     static constexpr int TILE_BYTES = 128 * D * 2;
     static constexpr int NSTAGE = D == 128 ? 4 : 8;
-    static constexpr int NBUF = 6;                            // logit tiles of half a streamed tile
-    static constexpr uint32_t TMEM_A = NBUF * 64;             // the item's rows: two buffers of D / 2 columns
+    static constexpr uint32_t TMEM_A = 256;                   // the item's rows: two buffers of two tiles of D / 2 columns
     static constexpr uint32_t TMEM_COLS = 512;
     static constexpr int SMEM = (2 + NSTAGE) * TILE_BYTES + 1024;
-    // A warpgroup waits for a buffer's next filling after it has seen a later one
-    // of the other buffers than the last filling (a barrier's parity repeats): as
-    // many buffers as warpgroups at least, filled in order by each issuer.
-    static constexpr int NWG = 4;
-    static_assert(NBUF >= NWG, "see above");
+    static constexpr int NWG = 4;                             // and logit tiles: warpgroup 2 m + h has item half m, tile half h
     static constexpr int W_EPI = 3, W_LOAD = W_EPI + 4 * NWG, W_OUT = W_LOAD + 4;   // first warps of the roles
-    static constexpr int NTABLE = 4;                          // tables a warpgroup
+    static constexpr int NTABLE = 4;                          // tables a tile half
     static constexpr int NSLOT = 4;                           // items whose sums wait for the writer
     static constexpr int THREADS = 32 * (W_OUT + 1);
-    static_assert(TMEM_A + D <= TMEM_COLS, "logit tiles and the items' rows fit");
+    static_assert(TMEM_A + 2 * D <= TMEM_COLS, "logit tiles and the items' rows fit");
 };
 
 // ---------------------------------------------------------------- the list of tiles
 // Within one (batch, key head): `own` items, item t streaming count(t) tiles.
-// With o = ceil((N_K - N_Q) / 128) (no causal mask: beyond every tile),
-//   kKeyMass: key tile t is seen by row tiles max(0, t - o) .. R - 1 of each head;
-//   kRowLse:  row tile r sees key tiles 0 .. min(A, r + 1 + o) - 1, A those with a key.
+// With o = ceil((N_K - N_Q) / 128) (no causal mask: beyond every tile), in tiles of 128,
+//   kKeyMass: keys 256 t .. are seen by row tiles max(0, 2 t - o) .. R - 1 of each head;
+//   kRowLse:  row tiles 2 r, 2 r + 1 see key tiles 0 .. min(A, 2 r + 2 + o) - 1, A those with
+//             a key; heads (or groups of packed heads) of one tile are taken in pairs.
 template <int MODE>
 struct TileList {
-    int own, A, o, R, mult;      // R: tiles a head; mult: heads (or packed groups of heads)
+    int own, A, o, R, mult;      // R: kKeyMass tiles, kRowLse items a head; mult: heads (or packed groups of heads)
     __device__ __forceinline__ TileList(const StatParams &p, int nk) {
+        const bool one = p.pack || p.R == 1;                  // tile a head
         A = (nk + 127) / 128;
-        R = p.pack ? 1 : p.R;
-        o = p.causal && !(MODE == kRowLse && p.pack) ? (p.N_K - p.N_Q + 127) / 128 : (1 << 28);
+        R = p.pack ? 1 : (MODE == kKeyMass ? p.R : (p.R + 1) / 2);
+        o = p.causal && !(MODE == kRowLse && one) ? (p.N_K - p.N_Q + 127) / 128 : (1 << 28);
         mult = p.pack ? p.R : p.G;
-        own = MODE == kKeyMass ? A : mult * R;
+        own = MODE == kKeyMass ? (nk + 255) / 256 : (one ? (mult + 1) / 2 : mult * R);
     }
-    // r: t (kKeyMass), the tile of its head (kRowLse)
+    // r: t (kKeyMass), the item of its head (kRowLse)
     __device__ __forceinline__ int count(int r) const {
-        return MODE == kKeyMass ? mult * (R - max(0, r - o)) : min(A, r + 1 + o);
+        return MODE == kKeyMass ? mult * (R - max(0, 2 * r - o)) : min(A, 2 * r + 2 + o);
     }
-    __device__ __forceinline__ long long before_row(int r) const {       // tiles of the row tiles before r of a head
-        const long long x = min(max(A - 1 - o, 0), r);
-        return x * (x + 1) / 2 + x * o + (r - x) * A;
+    __device__ __forceinline__ long long before_row(int r) const {       // tiles of the items before r of a head
+        const long long x = min(max((A - o - 1) >> 1, 0), r);
+        return x * (x + 1 + o) + (r - x) * A;
     }
     __device__ __forceinline__ long long before(int t) const {           // tiles of the items before t
         if (MODE == kKeyMass) {
-            const long long x = max(t - o, 0);
-            return ((long long)R * t - x * (x - 1) / 2) * mult;
+            const long long t1 = min(o / 2 + 1, t), x = t - t1;          // from t1 on, 2 t > o
+            return ((long long)R * t - x * (t1 + t - 1 - o)) * mult;
         }
         return (t / R) * before_row(R) + before_row(t % R);
     }
@@ -242,7 +239,7 @@ __device__ __forceinline__ RowTile row_tile(const StatParams &p, int hk, int q) 
 struct RowCursor {
     int g, r, first;             // head of the group (packed: group of heads), tile of it, first tile that sees the keys
     __device__ __forceinline__ RowCursor(const StatParams &p, const StatItem &it, int u) {
-        first = p.causal && !p.pack ? max(0, it.t - (p.N_K - p.N_Q + 127) / 128) : 0;
+        first = p.causal && !p.pack ? max(0, 2 * it.t - (p.N_K - p.N_Q + 127) / 128) : 0;
         const int per = p.pack ? 1 : p.R - first;
         g = per == 1 ? u : u / per;
         r = first + u - g * per;
@@ -277,8 +274,7 @@ __device__ __forceinline__ void tma_load_rows(void *dst, const CUtensorMap *map,
 // A tile of 128 rows, or (packed) of whole heads: one box, or one a block of 64 columns.
 template <int D>
 __device__ __forceinline__ void load_tile(uint8_t *dst, const CUtensorMap *map, uint64_t *bar, int row0, int head, int b,
-                                          int rows, int pack, int n_rows, int n_heads, int n_b, uint32_t *word) {
-    mbar_expect_tx(bar, rows * D * 2);
+                                          int pack, int n_rows, int n_heads, int n_b, uint32_t *word) {
     tma_load_rows(dst, map, bar, row0, head, 0, b, n_rows, n_heads, D / 64, n_b, word);
     if (D > 64 && pack)
         tma_load_rows(dst + StatCfg<D>::BOX, map, bar, row0, head, 1, b, n_rows, n_heads, D / 64, n_b, word);
@@ -373,15 +369,32 @@ __device__ __forceinline__ float mass_chunk(const float (&u)[W], float c, const 
     return t.x + t.y;
 }
 
+// Half m of an item: its query tile (kRowLse), whether it has rows at all.
+__device__ __forceinline__ bool item_rows(const StatParams &p, const StatItem &it, int m, RowTile &rt) {
+    if (p.pack || p.R == 1) {
+        const int q = 2 * it.t + m;
+        if (q >= (p.pack ? p.R : p.G)) return false;
+        rt = row_tile(p, it.hk, q);
+        return true;
+    }
+    const int per = (p.R + 1) / 2, g = it.t / per, r = 2 * (it.t - g * per) + m;
+    if (r >= p.R) return false;
+    rt = row_tile(p, it.hk, g * p.R + r);
+    return true;
+}
+
 // The owned row `row` of an item: where its result goes (in mass or lse), or
-// -1; in kRowLse also its position in its head.
+// -1; `i`: the key, or the row of its head.
 template <int MODE>
 __device__ __forceinline__ long long stat_out(const StatParams &p, const StatItem &it, int row, int &i) {
     if (MODE == kKeyMass) {
-        i = it.t * 128 + row;
+        i = it.t * 256 + row;
         return i < p.N_K ? ((long long)it.b * p.Hk + it.hk) * p.N_K + i : -1;
     }
-    const RowTile rt = row_tile(p, it.hk, it.t);
+    RowTile rt;
+    i = 0;
+    if (!item_rows(p, it, row >> 7, rt)) return -1;
+    row &= 127;
     const int g = p.pack ? row / p.N_Q : 0;
     i = rt.row0 + row - g * p.N_Q;
     return row < rt.rows ? ((long long)it.b * p.H + rt.head + g) * p.N_Q + i : -1;
@@ -396,27 +409,27 @@ __global__ void __launch_bounds__(StatCfg<D>::THREADS, 1)
     uint8_t *sA = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *sT = sA + 2 * C::TILE_BYTES;
 
-    __shared__ uint64_t bar_afull[2], bar_afree[2], bar_aready[2], bar_aempty[2];   // rows in smem, in tensor memory
+    __shared__ uint64_t bar_afull, bar_afree, bar_aready[2], bar_aempty[2];         // rows in smem, in tensor memory
     __shared__ uint64_t bar_full[C::NSTAGE], bar_empty[C::NSTAGE];
-    __shared__ uint64_t bar_sfull[C::NBUF], bar_sempty[C::NBUF], bar_ifull[C::NSLOT], bar_iempty[C::NSLOT];
+    __shared__ uint64_t bar_sfull[C::NWG], bar_sempty[C::NWG], bar_ifull[C::NSLOT], bar_iempty[C::NSLOT];
     __shared__ uint64_t bar_quiet[2];
     __shared__ uint32_t tmem_base_sh;
     __shared__ int abort_flag;
     __shared__ int rec[5];
     // kKeyMass: a half's rows: -lse * log2(e), the first, and how many there are | chunks with rows to leave out << 8
-    __shared__ uint64_t bar_tfull[C::NWG][C::NTABLE], bar_tempty[C::NWG][C::NTABLE];
-    __shared__ __align__(16) float table[C::NWG][C::NTABLE][64];
-    __shared__ int2 table_rows[C::NWG][C::NTABLE];
-    __shared__ float sums[C::NSLOT][C::NWG][MODE == kRowLse ? 2 : 1][C::BM];
+    __shared__ uint64_t bar_tfull[2][C::NTABLE], bar_tempty[2][C::NTABLE];
+    __shared__ __align__(16) float table[2][C::NTABLE][64];
+    __shared__ int2 table_rows[2][C::NTABLE];
+    __shared__ float sums[C::NSLOT][C::NWG][MODE == kRowLse ? 2 : 1][128];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int off = p.N_K - p.N_Q;
 
     grid_release();
     if (threadIdx.x == 0) {
+        mbar_init(&bar_afull, 1);
+        mbar_init(&bar_afree, 4);
         for (int s = 0; s < 2; ++s) {
-            mbar_init(&bar_afull[s], 1);
-            mbar_init(&bar_afree[s], 4);
             mbar_init(&bar_aready[s], 4);
             mbar_init(&bar_aempty[s], p.halves);
         }
@@ -424,7 +437,7 @@ __global__ void __launch_bounds__(StatCfg<D>::THREADS, 1)
             mbar_init(&bar_full[s], 1);
             mbar_init(&bar_empty[s], p.halves);
         }
-        for (int s = 0; s < C::NBUF; ++s) {
+        for (int s = 0; s < C::NWG; ++s) {
             mbar_init(&bar_sfull[s], 1);
             mbar_init(&bar_sempty[s], 4);
         }
@@ -432,9 +445,9 @@ __global__ void __launch_bounds__(StatCfg<D>::THREADS, 1)
             mbar_init(&bar_ifull[s], 4 * C::NWG);
             mbar_init(&bar_iempty[s], 1);
         }
-        for (int s = 0; s < C::NWG * C::NTABLE; ++s) {
+        for (int s = 0; s < 2 * C::NTABLE; ++s) {
             mbar_init(&bar_tfull[0][s], 1);
-            mbar_init(&bar_tempty[0][s], 4);
+            mbar_init(&bar_tempty[0][s], 8);                  // the warps of both item halves
         }
         mbar_init(&bar_quiet[0], 1);
         mbar_init(&bar_quiet[1], 1);
@@ -474,16 +487,23 @@ __global__ void __launch_bounds__(StatCfg<D>::THREADS, 1)
             const int q_rows = p.pack ? p.pack * p.N_Q : 128; // of a box
             for (; ok && iter.more(); iter.next(p), ++n_item) {
                 const StatItem &it = iter.it;
-                const int a = n_item & 1;
-                ok = n_item < 2 || long_wait(&bar_afree[a], ((n_item >> 1) - 1) & 1, p.st, abort_v, 1);
+                ok = n_item == 0 || long_wait(&bar_afree, (n_item - 1) & 1, p.st, abort_v, 1);
                 if (!ok) break;
-                uint8_t *dst = sA + a * C::TILE_BYTES;
+                uint8_t *dst = sA;
+                RowTile r0 = {0, 0, 0}, r1 = r0;
+                const bool two = MODE == kKeyMass ? it.t * 256 + 128 < p.N_K : item_rows(p, it, 1, r1);
+                mbar_expect_tx(&bar_afull, (two ? 2 : 1) * (MODE == kKeyMass ? 128 : q_rows) * D * 2);
                 if (MODE == kKeyMass) {
-                    load_tile<D>(dst, &mK, &bar_afull[a], it.t * 128, it.hk, it.b, 128, 0, p.N_K, p.Hk, p.B, p.st.word);
+                    load_tile<D>(dst, &mK, &bar_afull, it.t * 256, it.hk, it.b, 0, p.N_K, p.Hk, p.B, p.st.word);
+                    if (two)
+                        load_tile<D>(dst + C::TILE_BYTES, &mK, &bar_afull, it.t * 256 + 128, it.hk, it.b, 0, p.N_K, p.Hk,
+                                     p.B, p.st.word);
                 } else {
-                    const RowTile rt = row_tile(p, it.hk, it.t);
-                    load_tile<D>(dst, &mQ, &bar_afull[a], rt.row0, rt.head, it.b, q_rows, p.pack, p.N_Q, p.H, p.B,
-                                 p.st.word);
+                    item_rows(p, it, 0, r0);
+                    load_tile<D>(dst, &mQ, &bar_afull, r0.row0, r0.head, it.b, p.pack, p.N_Q, p.H, p.B, p.st.word);
+                    if (two)
+                        load_tile<D>(dst + C::TILE_BYTES, &mQ, &bar_afull, r1.row0, r1.head, it.b, p.pack, p.N_Q, p.H,
+                                     p.B, p.st.word);
                 }
                 ++a_asked;
                 RowCursor cur(p, it, MODE == kKeyMass ? it.lo : 0);
@@ -495,10 +515,11 @@ __global__ void __launch_bounds__(StatCfg<D>::THREADS, 1)
                     if (MODE == kKeyMass) {
                         const RowTile rt = cur.tile(p, it.hk);
                         cur.advance(p, 1);
-                        load_tile<D>(dst, &mQ, &bar_full[s], rt.row0, rt.head, it.b, q_rows, p.pack, p.N_Q, p.H, p.B,
-                                     p.st.word);
+                        mbar_expect_tx(&bar_full[s], q_rows * D * 2);
+                        load_tile<D>(dst, &mQ, &bar_full[s], rt.row0, rt.head, it.b, p.pack, p.N_Q, p.H, p.B, p.st.word);
                     } else {
-                        load_tile<D>(dst, &mK, &bar_full[s], u * 128, it.hk, it.b, 128, 0, p.N_K, p.Hk, p.B, p.st.word);
+                        mbar_expect_tx(&bar_full[s], 128 * D * 2);
+                        load_tile<D>(dst, &mK, &bar_full[s], u * 128, it.hk, it.b, 0, p.N_K, p.Hk, p.B, p.st.word);
                     }
                 }
             }
@@ -509,8 +530,7 @@ __global__ void __launch_bounds__(StatCfg<D>::THREADS, 1)
                 volatile int never = 0;
                 for (int s = max(0, t - C::NSTAGE); s < t; ++s)
                     mbar_wait(&bar_full[s % C::NSTAGE], (s / C::NSTAGE) & 1, quick, &never, 2);
-                for (int s = max(0, a_asked - 2); s < a_asked; ++s)
-                    mbar_wait(&bar_afull[s & 1], (s >> 1) & 1, quick, &never, 1);
+                if (a_asked > 0) mbar_wait(&bar_afull, (a_asked - 1) & 1, quick, &never, 1);
             }
         }
     } else if (warp < C::W_EPI) {
@@ -518,27 +538,30 @@ __global__ void __launch_bounds__(StatCfg<D>::THREADS, 1)
         const int half = warp - 1;
         if (half < p.halves && elect_one()) {
             const uint64_t t0 = sw128_desc(smem_u32(sT) + half * 64 * 128, 16, 1024);
-            const uint32_t id = p.fp16 ? idesc_fp16(C::BM, 64, 0, 0) : idesc_bf16(C::BM, 64, 0, 0);
-            int n_item = 0, s = 0, ps = 0, hb = half, use = 0;
+            const uint32_t id = p.fp16 ? idesc_fp16(128, 64, 0, 0) : idesc_bf16(128, 64, 0, 0);
+            int n_item = 0, s = 0, ps = 0, t = 0;
             bool ok = true;
             for (; ok && iter.more(); iter.next(p), ++n_item) {
                 const int a = n_item & 1;
                 if (!long_wait(&bar_aready[a], (n_item >> 1) & 1, p.st, abort_v, 3)) break;
-                const uint32_t ta = tmem + C::TMEM_A + a * (D / 2);
-                for (int u = 0; u < iter.it.n; ++u) {
-                    ok = (use == 0 || long_wait(&bar_sempty[hb], (use - 1) & 1, p.st, abort_v, 5)) &&
-                         long_wait(&bar_full[s], ps, p.st, abort_v, 4);
-                    if (!ok) break;
-                    tc_fence_after();
+                const uint32_t ta = tmem + C::TMEM_A + a * D;
+                for (int u = 0; u < iter.it.n; ++u, ++t) {
+                    if (!(ok = long_wait(&bar_full[s], ps, p.st, abort_v, 4))) break;
                     const uint64_t dt = desc_add(t0, s * C::TILE_BYTES);
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk)
-                        mma_bf16_ts(tmem + hb * 64, ta + kk * 8, desc_add(dt, (kk >> 2) * C::BOX + (kk & 3) * 32), id,
-                                    kk > 0);
-                    mma_commit(&bar_sfull[hb]);
+                    for (int m = 0; m < 2; ++m) {
+                        const int buf = 2 * m + half;
+                        if (!(ok = t == 0 || long_wait(&bar_sempty[buf], (t - 1) & 1, p.st, abort_v, 5))) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk)
+                            mma_bf16_ts(tmem + buf * 64, ta + m * (D / 2) + kk * 8,
+                                        desc_add(dt, (kk >> 2) * C::BOX + (kk & 3) * 32), id, kk > 0);
+                        mma_commit(&bar_sfull[buf]);
+                    }
+                    if (!ok) break;
                     mma_commit(&bar_empty[s]);
                     if (++s == C::NSTAGE) { s = 0; ps ^= 1; }
-                    if ((hb += p.halves) >= C::NBUF) { hb -= C::NBUF; ++use; }
                 }
                 if (ok) mma_commit(&bar_aempty[a]);
             }
@@ -546,35 +569,33 @@ __global__ void __launch_bounds__(StatCfg<D>::THREADS, 1)
         }
     } else if (warp < C::W_LOAD) {
         // ------------------------------------------------------------ owned rows
-        const int wg = (warp - C::W_EPI) >> 2, sub = warp & 3, row = sub * 32 + lane;
-        const uint32_t lane_base = tmem + ((uint32_t)(sub * 32) << 16);
-        // halves in turn: half index 2 t + half (or t) of the run goes to warpgroup index mod 4
-        const int step = C::NWG / p.halves, phase = wg / p.halves, half = wg % p.halves;
-        int n_item = 0, t = 0, e = 0, pe = 0;                 // t: tiles before this item; e, pe: table, its parity
+        const int wg = (warp - C::W_EPI) >> 2, m = wg >> 1, half = wg & 1, sub = warp & 3;
+        const int lrow = sub * 32 + lane, row = m * 128 + lrow;
+        const uint32_t logits = tmem + ((uint32_t)(sub * 32) << 16) + wg * 64;
+        int n_item = 0, t = 0, e = 0, pe = 0;                 // t: tiles so far; e, pe: table, its parity
         bool ok = true;
-        for (; ok && iter.more(); t += iter.it.n, iter.next(p), ++n_item) {
+        for (; ok && iter.more(); iter.next(p), ++n_item) {
             const StatItem &it = iter.it;
             int i, lim = 0;                                   // lim: first hidden key (rows past the tile's end see none)
-            if (stat_out<MODE>(p, it, row, i) >= 0 && MODE == kRowLse) lim = p.causal ? min(it.nk, i + off + 1) : it.nk;
+            const bool mine = stat_out<MODE>(p, it, row, i) >= 0;
+            if (mine && MODE == kRowLse) lim = p.causal ? min(it.nk, i + off + 1) : it.nk;
+            const bool idle = !__any_sync(0xffffffffu, mine); // nothing of the item is this warp's
             // row i sees key j iff i >= j - off: of a head's rows, those from `first` on; `last`: the tile's largest
             const int first = MODE == kKeyMass && p.causal ? i - off : 0;
-            const int last = MODE == kKeyMass && p.causal ? it.t * 128 + 127 - off : 0;
+            const int last = MODE == kKeyMass && p.causal ? it.t * 256 + m * 128 + 127 - off : 0;
             float M = -INFINITY, l = 0.f;
-            for (int x = (phase - t) & (step - 1); x < it.n; x += step) {
-                const int tt = t + x;
-                if (MODE == kKeyMass) ok = warp_wait(&bar_tfull[wg][e], pe, p.st, abort_v, 12);
-                const int hc = tt * p.halves + half, buf = hc % C::NBUF;
-                const int2 info = MODE == kKeyMass ? table_rows[wg][e] : make_int2(0, 64);
-                const float *tab = table[wg][e];
-                const int row0 = info.x, chunks = ((info.y & 255) + 31) >> 5;
-                ok = ok && warp_wait(&bar_sfull[buf], (hc / C::NBUF) & 1, p.st, abort_v, 6);
+            for (int x = half < p.halves ? 0 : it.n; x < it.n; ++x, ++t) {
+                if (MODE == kKeyMass) ok = warp_wait(&bar_tfull[half][e], pe, p.st, abort_v, 12);
+                const int2 info = MODE == kKeyMass ? table_rows[half][e] : make_int2(0, 64);
+                const float *tab = table[half][e];
+                const int row0 = info.x, chunks = idle ? 0 : ((info.y & 255) + 31) >> 5;
+                ok = ok && warp_wait(&bar_sfull[wg], t & 1, p.st, abort_v, 6);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t logits = lane_base + buf * 64;
                 auto release = [&]() {                        // the logits are read
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar_sempty[buf]);
+                    if (lane == 0) mbar_arrive(&bar_sempty[wg]);
                 };
                 // two bodies: masks in the common one would cost copies of its registers
                 const int c0 = (it.lo + x) * C::BN + half * 64;              // kRowLse: the half's first key
@@ -600,6 +621,9 @@ __global__ void __launch_bounds__(StatCfg<D>::THREADS, 1)
                         tmem_ld32(logits + x2 * 32, u);
                         tmem_ld_wait();
                         const int r0 = row0 + x2 * 32;
+                        if (MODE == kRowLse ? __all_sync(0xffffffffu, c0 + x2 * 32 >= lim)
+                                            : !p.pack && last - 127 - r0 >= 32)
+                            continue;                         // nothing seen
                         int h = MODE == kRowLse ? lim - c0 - x2 * 32 : first - r0;   // keys below h are seen; rows from h on see
                         if (MODE == kKeyMass && last <= (p.pack ? 0 : r0)) {
                             // every row sees the keys
@@ -630,15 +654,15 @@ __global__ void __launch_bounds__(StatCfg<D>::THREADS, 1)
                 }
                 if (MODE == kKeyMass) {
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar_tempty[wg][e]);
+                    if (lane == 0) mbar_arrive(&bar_tempty[half][e]);
                     if (++e == C::NTABLE) { e = 0; pe ^= 1; }
                 }
             }
             const int slot = n_item % C::NSLOT, use = n_item / C::NSLOT;
             ok = ok && (use == 0 || warp_wait(&bar_iempty[slot], (use - 1) & 1, p.st, abort_v, 8));
             if (!ok) break;
-            sums[slot][wg][0][row] = l;
-            if (MODE == kRowLse) sums[slot][wg][1][row] = M;
+            sums[slot][wg][0][lrow] = l;
+            if (MODE == kRowLse) sums[slot][wg][1][lrow] = M;
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar_ifull[slot]);
         }
@@ -646,37 +670,39 @@ __global__ void __launch_bounds__(StatCfg<D>::THREADS, 1)
         // ------------------------------------------------------------ rows to tensor memory
         const int sub = warp & 3, row = sub * 32 + lane;
         const uint32_t dst = tmem + ((uint32_t)(sub * 32) << 16) + C::TMEM_A;
-        // tables for warpgroup `wg`
-        const int wg = warp - C::W_LOAD, step = C::NWG / p.halves, phase = wg / p.halves, half = wg % p.halves;
+        const int half = warp - C::W_LOAD;                    // 0, 1: the tables of that half
         bool ok = true;
-        for (int n_item = 0, t = 0, e = 0, use_e = 0; ok && iter.more(); t += iter.it.n, iter.next(p), ++n_item) {
+        for (int n_item = 0, e = 0, use_e = 0; ok && iter.more(); iter.next(p), ++n_item) {
             const int a = n_item & 1, use = n_item >> 1;
-            if (!warp_wait(&bar_afull[a], use & 1, p.st, abort_v, 7)) break;
+            if (!warp_wait(&bar_afull, n_item & 1, p.st, abort_v, 7)) break;
             if (use > 0 && !warp_wait(&bar_aempty[a], (use - 1) & 1, p.st, abort_v, 11)) break;
             tc_fence_after();
-            const uint8_t *src = sA + a * C::TILE_BYTES;
+#pragma unroll 1
+            for (int m = 0; m < 2; ++m) {
+                const uint8_t *src = sA + m * C::TILE_BYTES;
 #pragma unroll
-            for (int x = 0; x < D / 32; ++x) {                // 32 elements, 16 columns
-                uint32_t v[16];
+                for (int x = 0; x < D / 32; ++x) {            // 32 elements, 16 columns
+                    uint32_t v[16];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int e = x * 32 + k * 8;
-                    const uint4 q = *reinterpret_cast<const uint4 *>(src + (e / 64) * C::BOX + sw128_offset(row, e % 64));
-                    v[4 * k] = q.x; v[4 * k + 1] = q.y; v[4 * k + 2] = q.z; v[4 * k + 3] = q.w;
+                    for (int k = 0; k < 4; ++k) {
+                        const int c = x * 32 + k * 8;
+                        const uint4 q =
+                            *reinterpret_cast<const uint4 *>(src + (c / 64) * C::BOX + sw128_offset(row, c % 64));
+                        v[4 * k] = q.x; v[4 * k + 1] = q.y; v[4 * k + 2] = q.z; v[4 * k + 3] = q.w;
+                    }
+                    tmem_st16(dst + a * D + m * (D / 2) + x * 16, v);
                 }
-                tmem_st16(dst + a * (D / 2) + x * 16, v);
             }
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(&bar_afree[a]);
+                mbar_arrive(&bar_afree);
                 mbar_arrive(&bar_aready[a]);
             }
-            if (MODE != kKeyMass) continue;
+            if (MODE != kKeyMass || half >= p.halves) continue;
             const StatItem &it = iter.it;
-            const int x0 = (phase - t) & (step - 1);
-            RowCursor cur(p, it, it.lo + x0);
+            RowCursor cur(p, it, it.lo);
             RowTile rt = {0, 0, 0};
             float ahead[2];                                   // log-sum-exps of the half's rows (packed heads follow)
             auto load_lse = [&]() {
@@ -688,8 +714,8 @@ __global__ void __launch_bounds__(StatCfg<D>::THREADS, 1)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) ahead[k] = in && k * 32 + lane < rt.rows ? lse[k * 32 + lane] : 0.f;
             };
-            if (x0 < it.n) load_lse();
-            for (int x = x0; x < it.n; x += step) {
+            load_lse();
+            for (int x = 0; x < it.n; ++x) {
                 float nb[2];
                 int rows = rt.rows;
                 const int row0 = rt.row0;
@@ -700,17 +726,17 @@ __global__ void __launch_bounds__(StatCfg<D>::THREADS, 1)
                     // (rows past a head's end are zeros, those past packed heads are not)
                     if (__any_sync(0xffffffffu, in ? none : p.pack > 0)) rows |= 256 << k;
                 }
-                if (x + step < it.n) {
-                    cur.advance(p, step);
+                if (x + 1 < it.n) {
+                    cur.advance(p, 1);
                     load_lse();
                 }
-                ok = use_e == 0 || warp_wait(&bar_tempty[wg][e], (use_e - 1) & 1, p.st, abort_v, 13);
+                ok = use_e == 0 || warp_wait(&bar_tempty[half][e], (use_e - 1) & 1, p.st, abort_v, 13);
                 if (!ok) break;
-                table[wg][e][lane] = nb[0];
-                table[wg][e][32 + lane] = nb[1];
-                if (lane == 0) table_rows[wg][e] = make_int2(row0, rows);
+                table[half][e][lane] = nb[0];
+                table[half][e][32 + lane] = nb[1];
+                if (lane == 0) table_rows[half][e] = make_int2(row0, rows);
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar_tfull[wg][e]);
+                if (lane == 0) mbar_arrive(&bar_tfull[half][e]);
                 if (++e == C::NTABLE) { e = 0; ++use_e; }
             }
         }
@@ -723,14 +749,11 @@ __global__ void __launch_bounds__(StatCfg<D>::THREADS, 1)
             const bool whole = it.n == it.count;
             // an item that two runs share: this run's first item, or its last
             float *part = p.part + ((size_t)blockIdx.x * 2 + (n_item > 0 ? 1 : 0)) * 2 * C::BM;
-#pragma unroll
             for (int r = lane; r < C::BM; r += 32) {
-                float l = sums[slot][0][0][r], M = MODE == kRowLse ? sums[slot][0][1][r] : 0.f;
-#pragma unroll
-                for (int w = 1; w < C::NWG; ++w) {
-                    if (MODE == kRowLse) lse_join(M, l, sums[slot][w][1][r], sums[slot][w][0][r]);
-                    else l += sums[slot][w][0][r];
-                }
+                const int w = r >> 7 << 1, q = r & 127;       // the item half's first warpgroup
+                float l = sums[slot][w][0][q], M = MODE == kRowLse ? sums[slot][w][1][q] : 0.f;
+                if (MODE == kRowLse) lse_join(M, l, sums[slot][w + 1][1][q], sums[slot][w + 1][0][q]);
+                else l += sums[slot][w + 1][0][q];
                 int i;
                 const long long at = stat_out<MODE>(p, it, r, i);
                 if (MODE == kKeyMass && i >= it.nk) l = 0.f;  // keys past the length received nothing
@@ -749,14 +772,14 @@ __global__ void __launch_bounds__(StatCfg<D>::THREADS, 1)
         }
         // items without a tile (all keys of the batch element, or of the key tile, are padding)
         if (p.kv_len && !(MODE == kKeyMass && p.accumulate)) {
-            const int per = MODE == kKeyMass ? (p.N_K + 127) / 128 : p.R * (p.pack ? 1 : p.G);
+            const int per = MODE == kKeyMass ? (p.N_K + 255) / 256 : TileList<MODE>(p, p.N_K).own;
             for (long long x = blockIdx.x; x < (long long)p.B * p.Hk * per; x += gridDim.x) {
                 StatItem it;
                 it.t = (int)(x % per);
                 it.hk = (int)(x / per % p.Hk);
                 it.b = (int)(x / per / p.Hk);
                 it.nk = key_count(p.kv_len, it.b, p.N_K, p.st.word, false);
-                if (MODE == kKeyMass ? it.t * 128 < it.nk : it.nk > 0) continue;
+                if (MODE == kKeyMass ? it.t * 256 < it.nk : it.nk > 0) continue;
                 for (int r = lane; r < C::BM; r += 32) {
                     int i;
                     const long long at = stat_out<MODE>(p, it, r, i);
@@ -777,7 +800,7 @@ __global__ void __launch_bounds__(StatCfg<D>::THREADS, 1)
 // Joins the partial sums of the items that several runs share: block k the one
 // that the end of run k cuts, if it starts in that run.
 template <int MODE>
-__global__ void __launch_bounds__(128) streamkl_stat_finish_kernel(const StatParams p) {
+__global__ void __launch_bounds__(256) streamkl_stat_finish_kernel(const StatParams p) {
     __shared__ long long rec[5];
     grid_release();
     if (threadIdx.x < 32) {
@@ -804,8 +827,8 @@ __global__ void __launch_bounds__(128) streamkl_stat_finish_kernel(const StatPar
     float sum = 0.f, M = -INFINITY;
     for (int c = c0; c <= c1; ++c) {
         // it is the first item of a run unless it starts inside
-        const float *part = p.part + ((size_t)c * 2 + (c == c0 && start > c * run ? 1 : 0)) * 2 * 128;
-        if (MODE == kRowLse) lse_join(M, sum, part[128 + r], part[r]);
+        const float *part = p.part + ((size_t)c * 2 + (c == c0 && start > c * run ? 1 : 0)) * 2 * 256;
+        if (MODE == kRowLse) lse_join(M, sum, part[256 + r], part[r]);
         else sum += part[r];
     }
     int i;
