@@ -104,8 +104,8 @@ streamkl_status launch_stat(const void *q, const long long *qs, const void *k, c
     auto kern = streamkl_stat_kernel<D, MODE>;
     if (set_smem(kern, C::SMEM) != cudaSuccess) return STREAMKL_ERR_CUDA;
     streamkl_status st = launch_ex(kern, p.grid, C::THREADS, C::SMEM, s, dependent, 1, mq, mk, p);
-    if (st != STREAMKL_OK || p.grid == 1) return st;
-    return launch_ex(streamkl_stat_finish_kernel<MODE>, p.grid - 1, 256, 0, s, true, 1, p);
+    if (st != STREAMKL_OK || (p.grid == 1 && !p.kv_len)) return st;
+    return launch_ex(streamkl_stat_finish_kernel<MODE>, std::max(1, p.grid - 1), 256, 0, s, true, 1, p);
 }
 
 bool paged_shape_ok(int B, int H, int H_k, int num_pages, int page_size, int max_pages, int dtype) {

@@ -25,10 +25,10 @@
 //               tile from shared memory (with A in shared memory too, 128 x 128
 //               logits took 870 clocks of its bandwidth instead of 512).
 //   warps 3..18 four warpgroups, one a logit tile; thread = owned row.
-//   warps 19..22 copy an item's rows from shared to tensor memory, an item ahead;
-//               in kKeyMass two of them write the -lse * log2(e) of a half's rows
-//               as a table for the warpgroups.
-//   warp 23     adds the warpgroups' sums of an item and writes it.
+//   warps 19..22 copy an item's rows from shared to tensor memory, an item ahead,
+//               and add and write the warpgroups' sums of an item.
+//   warp 23     in kKeyMass writes the -lse * log2(e) of a tile's rows as tables for
+//               the warpgroups.
 // Work bound: one exponential a pair (16 a clock and SM: 2048 clocks a tile)
 // against 2 d flops (1024 clocks a tile at d = 128) and 32 KB of streamed rows
 // from L2 (items of 128 rows read them twice as often, 9 TB/s over all SMs).
@@ -67,10 +67,10 @@ struct StatCfg {
     static constexpr uint32_t TMEM_COLS = 512;
     static constexpr int SMEM = (2 + NSTAGE) * TILE_BYTES + 1024;
     static constexpr int NWG = 4;                             // and logit tiles: warpgroup 2 m + h has item half m, tile half h
-    static constexpr int W_EPI = 3, W_LOAD = W_EPI + 4 * NWG, W_OUT = W_LOAD + 4;   // first warps of the roles
+    static constexpr int W_EPI = 3, W_LOAD = W_EPI + 4 * NWG, W_TABLE = W_LOAD + 4; // first warps of the roles
     static constexpr int NTABLE = 4;                          // tables a tile half
     static constexpr int NSLOT = 4;                           // items whose sums wait for the writer
-    static constexpr int THREADS = 32 * (W_OUT + 1);
+    static constexpr int THREADS = 32 * (W_TABLE + 1);
     static_assert(TMEM_A + 2 * D <= TMEM_COLS, "logit tiles and the items' rows fit");
 };
 
@@ -280,38 +280,12 @@ __device__ __forceinline__ void load_tile(uint8_t *dst, const CUtensorMap *map, 
         tma_load_rows(dst + StatCfg<D>::BOX, map, bar, row0, head, 1, b, n_rows, n_heads, D / 64, n_b, word);
 }
 
-// mbar_wait for the long waits of this kernel's roles: the thread is suspended
-// up to 10 us at a time instead of polling (ten roles' polls took two thirds of
-// the issued instructions, and shared memory's queue from the exponentials).
-__device__ __forceinline__ bool try_wait_long(uint64_t *bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 10000;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-__device__ __forceinline__ bool long_wait(uint64_t *bar, uint32_t parity, const DevStatus &st, volatile int *abort_flag,
-                                          uint32_t who) {
-    if (try_wait_long(bar, parity)) return true;
-    const unsigned long long t0 = globaltimer();
-    for (;;) {
-        if (try_wait_long(bar, parity)) return true;
-        if (*abort_flag) return false;
-        if (globaltimer() - t0 > st.budget_ns) {
-            *abort_flag = 1;
-            if (st.word) atomicOr(st.word, kStatusTimeout | (who << kStatusWhoShift));
-            return false;
-        }
-    }
-}
-// The same by a whole warp, whose lanes take the same way out.
+// mbar_wait by a whole warp, whose lanes take the same way out.  (One lane
+// waiting for the warp took 50 us more of 320: the exchange costs more than 32
+// lanes' waits.)
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const DevStatus &st, volatile int *abort_flag,
                                           uint32_t who) {
-    return __all_sync(0xffffffffu, long_wait(bar, parity, st, abort_flag, who));
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, st, abort_flag, who));
 }
 
 // Online log-sum-exp state of one row: M the running maximum (log2 units), l
@@ -443,7 +417,7 @@ __global__ void __launch_bounds__(StatCfg<D>::THREADS, 1)
         }
         for (int s = 0; s < C::NSLOT; ++s) {
             mbar_init(&bar_ifull[s], 4 * C::NWG);
-            mbar_init(&bar_iempty[s], 1);
+            mbar_init(&bar_iempty[s], 4);
         }
         for (int s = 0; s < 2 * C::NTABLE; ++s) {
             mbar_init(&bar_tfull[0][s], 1);
@@ -487,7 +461,7 @@ __global__ void __launch_bounds__(StatCfg<D>::THREADS, 1)
             const int q_rows = p.pack ? p.pack * p.N_Q : 128; // of a box
             for (; ok && iter.more(); iter.next(p), ++n_item) {
                 const StatItem &it = iter.it;
-                ok = n_item == 0 || long_wait(&bar_afree, (n_item - 1) & 1, p.st, abort_v, 1);
+                ok = n_item == 0 || mbar_wait(&bar_afree, (n_item - 1) & 1, p.st, abort_v, 1);
                 if (!ok) break;
                 uint8_t *dst = sA;
                 RowTile r0 = {0, 0, 0}, r1 = r0;
@@ -509,7 +483,7 @@ __global__ void __launch_bounds__(StatCfg<D>::THREADS, 1)
                 RowCursor cur(p, it, MODE == kKeyMass ? it.lo : 0);
                 for (int u = it.lo; u < it.lo + it.n; ++u, ++t) {
                     const int s = t % C::NSTAGE, n = t / C::NSTAGE;
-                    ok = n == 0 || long_wait(&bar_empty[s], (n - 1) & 1, p.st, abort_v, 2);
+                    ok = n == 0 || mbar_wait(&bar_empty[s], (n - 1) & 1, p.st, abort_v, 2);
                     if (!ok) break;
                     dst = sT + s * C::TILE_BYTES;
                     if (MODE == kKeyMass) {
@@ -543,15 +517,15 @@ __global__ void __launch_bounds__(StatCfg<D>::THREADS, 1)
             bool ok = true;
             for (; ok && iter.more(); iter.next(p), ++n_item) {
                 const int a = n_item & 1;
-                if (!long_wait(&bar_aready[a], (n_item >> 1) & 1, p.st, abort_v, 3)) break;
+                if (!mbar_wait(&bar_aready[a], (n_item >> 1) & 1, p.st, abort_v, 3)) break;
                 const uint32_t ta = tmem + C::TMEM_A + a * D;
                 for (int u = 0; u < iter.it.n; ++u, ++t) {
-                    if (!(ok = long_wait(&bar_full[s], ps, p.st, abort_v, 4))) break;
+                    if (!(ok = mbar_wait(&bar_full[s], ps, p.st, abort_v, 4))) break;
                     const uint64_t dt = desc_add(t0, s * C::TILE_BYTES);
 #pragma unroll
                     for (int m = 0; m < 2; ++m) {
                         const int buf = 2 * m + half;
-                        if (!(ok = t == 0 || long_wait(&bar_sempty[buf], (t - 1) & 1, p.st, abort_v, 5))) break;
+                        if (!(ok = t == 0 || mbar_wait(&bar_sempty[buf], (t - 1) & 1, p.st, abort_v, 5))) break;
                         tc_fence_after();
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk)
@@ -666,16 +640,14 @@ __global__ void __launch_bounds__(StatCfg<D>::THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar_ifull[slot]);
         }
-    } else if (warp < C::W_OUT) {
-        // ------------------------------------------------------------ rows to tensor memory
+    } else if (warp < C::W_TABLE) {
+        // ------------------------------------------------------------ rows to tensor memory, sums out
         const int sub = warp & 3, row = sub * 32 + lane;
         const uint32_t dst = tmem + ((uint32_t)(sub * 32) << 16) + C::TMEM_A;
-        const int half = warp - C::W_LOAD;                    // 0, 1: the tables of that half
-        bool ok = true;
-        for (int n_item = 0, e = 0, use_e = 0; ok && iter.more(); iter.next(p), ++n_item) {
+        auto copy = [&](int n_item) -> bool {
             const int a = n_item & 1, use = n_item >> 1;
-            if (!warp_wait(&bar_afull, n_item & 1, p.st, abort_v, 7)) break;
-            if (use > 0 && !warp_wait(&bar_aempty[a], (use - 1) & 1, p.st, abort_v, 11)) break;
+            if (!warp_wait(&bar_afull, n_item & 1, p.st, abort_v, 7)) return false;
+            if (use > 0 && !warp_wait(&bar_aempty[a], (use - 1) & 1, p.st, abort_v, 11)) return false;
             tc_fence_after();
 #pragma unroll 1
             for (int m = 0; m < 2; ++m) {
@@ -700,57 +672,18 @@ __global__ void __launch_bounds__(StatCfg<D>::THREADS, 1)
                 mbar_arrive(&bar_afree);
                 mbar_arrive(&bar_aready[a]);
             }
-            if (MODE != kKeyMass || half >= p.halves) continue;
-            const StatItem &it = iter.it;
-            RowCursor cur(p, it, it.lo);
-            RowTile rt = {0, 0, 0};
-            float ahead[2];                                   // log-sum-exps of the half's rows (packed heads follow)
-            auto load_lse = [&]() {
-                rt = cur.tile(p, it.hk);
-                rt.row0 += half * 64;
-                rt.rows = max(0, min(rt.rows - half * 64, 64));
-                const float *lse = p.lse + ((size_t)it.b * p.H + rt.head) * p.N_Q + rt.row0;
-                const bool in = bound_ok(it.b < p.B && rt.head < p.H && rt.row0 >= 0, p.st.word, kSiteConst);
-#pragma unroll
-                for (int k = 0; k < 2; ++k) ahead[k] = in && k * 32 + lane < rt.rows ? lse[k * 32 + lane] : 0.f;
-            };
-            load_lse();
-            for (int x = 0; x < it.n; ++x) {
-                float nb[2];
-                int rows = rt.rows;
-                const int row0 = rt.row0;
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const bool in = k * 32 + lane < rt.rows, none = fabsf(ahead[k]) == INFINITY;
-                    nb[k] = in && !none ? -1.4426950408889634074f * ahead[k] : -INFINITY;
-                    // (rows past a head's end are zeros, those past packed heads are not)
-                    if (__any_sync(0xffffffffu, in ? none : p.pack > 0)) rows |= 256 << k;
-                }
-                if (x + 1 < it.n) {
-                    cur.advance(p, 1);
-                    load_lse();
-                }
-                ok = use_e == 0 || warp_wait(&bar_tempty[half][e], (use_e - 1) & 1, p.st, abort_v, 13);
-                if (!ok) break;
-                table[half][e][lane] = nb[0];
-                table[half][e][32 + lane] = nb[1];
-                if (lane == 0) table_rows[half][e] = make_int2(row0, rows);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar_tfull[half][e]);
-                if (++e == C::NTABLE) { e = 0; ++use_e; }
-            }
-        }
-    } else {
-        // ------------------------------------------------------------ writer
-        for (int n_item = 0; iter.more(); iter.next(p), ++n_item) {
-            const StatItem &it = iter.it;
+            return true;
+        };
+        // this warp's 64 rows of an item: the sums of two warpgroups
+        auto write = [&](const StatItem &it, int n_item) -> bool {
             const int slot = n_item % C::NSLOT;
-            if (!warp_wait(&bar_ifull[slot], (n_item / C::NSLOT) & 1, p.st, abort_v, 10)) break;
+            if (!warp_wait(&bar_ifull[slot], (n_item / C::NSLOT) & 1, p.st, abort_v, 10)) return false;
             const bool whole = it.n == it.count;
             // an item that two runs share: this run's first item, or its last
             float *part = p.part + ((size_t)blockIdx.x * 2 + (n_item > 0 ? 1 : 0)) * 2 * C::BM;
-            for (int r = lane; r < C::BM; r += 32) {
-                const int w = r >> 7 << 1, q = r & 127;       // the item half's first warpgroup
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int w = 2 * k, q = row, r = k * 128 + row;
                 float l = sums[slot][w][0][q], M = MODE == kRowLse ? sums[slot][w][1][q] : 0.f;
                 if (MODE == kRowLse) lse_join(M, l, sums[slot][w + 1][1][q], sums[slot][w + 1][0][q]);
                 else l += sums[slot][w + 1][0][q];
@@ -769,23 +702,63 @@ __global__ void __launch_bounds__(StatCfg<D>::THREADS, 1)
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar_iempty[slot]);
+            return true;
+        };
+        bool ok = !iter.more() || copy(0);
+        for (int n_item = 0; ok && iter.more(); ++n_item) {
+            const StatItem it = iter.it;
+            iter.next(p);
+            ok = (!iter.more() || copy(n_item + 1)) && write(it, n_item);
         }
-        // items without a tile (all keys of the batch element, or of the key tile, are padding)
-        if (p.kv_len && !(MODE == kKeyMass && p.accumulate)) {
-            const int per = MODE == kKeyMass ? (p.N_K + 255) / 256 : TileList<MODE>(p, p.N_K).own;
-            for (long long x = blockIdx.x; x < (long long)p.B * p.Hk * per; x += gridDim.x) {
-                StatItem it;
-                it.t = (int)(x % per);
-                it.hk = (int)(x / per % p.Hk);
-                it.b = (int)(x / per / p.Hk);
-                it.nk = key_count(p.kv_len, it.b, p.N_K, p.st.word, false);
-                if (MODE == kKeyMass ? it.t * 256 < it.nk : it.nk > 0) continue;
-                for (int r = lane; r < C::BM; r += 32) {
-                    int i;
-                    const long long at = stat_out<MODE>(p, it, r, i);
-                    if (at >= 0) (MODE == kKeyMass ? p.mass : p.lse)[at] = MODE == kKeyMass ? 0.f : -INFINITY;
-                }
+    } else if (MODE == kKeyMass) {
+        // ------------------------------------------------------------ tables
+        int e = 0, use_e = 0, x = 0;
+        float l[4];                                           // log-sum-exps of a tile's rows (packed heads follow)
+        RowTile rt = {0, 0, 0};
+        auto load_lse = [&](const RowCursor &cur) {
+            rt = cur.tile(p, iter.it.hk);
+            const float *lse = p.lse + ((size_t)iter.it.b * p.H + rt.head) * p.N_Q + rt.row0;
+            const bool in = bound_ok(iter.it.b < p.B && rt.head < p.H && rt.row0 >= 0, p.st.word, kSiteConst);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) l[k] = in && k * 32 + lane < rt.rows ? lse[k * 32 + lane] : 0.f;
+        };
+        RowCursor cur(p, iter.it, iter.it.lo);
+        bool more = iter.more();
+        if (more) load_lse(cur);
+        while (more) {
+            float nb[4];
+            uint32_t odd = 0u;
+            const int row0 = rt.row0, rows = rt.rows;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const bool in = k * 32 + lane < rows, none = fabsf(l[k]) == INFINITY;
+                nb[k] = in && !none ? -1.4426950408889634074f * l[k] : -INFINITY;
+                // (rows past a head's end are zeros, those past packed heads are not)
+                if (__any_sync(0xffffffffu, in ? none : p.pack > 0)) odd |= 1u << k;
             }
+            // the next tile's are loaded while this one's wait for their place
+            if (++x < iter.it.n) {
+                cur.advance(p, 1);
+            } else {
+                x = 0;
+                iter.next(p);
+                if ((more = iter.more())) cur = RowCursor(p, iter.it, iter.it.lo);
+            }
+            if (more) load_lse(cur);
+            for (int h = 0; h < p.halves; ++h) {
+                if (use_e > 0 && !warp_wait(&bar_tempty[h][e], (use_e - 1) & 1, p.st, abort_v, 13)) {
+                    more = false;
+                    break;
+                }
+                table[h][e][lane] = h ? nb[2] : nb[0];
+                table[h][e][32 + lane] = h ? nb[3] : nb[1];
+                if (lane == 0)
+                    table_rows[h][e] =
+                        make_int2(row0 + h * 64, max(0, min(rows - h * 64, 64)) | ((odd >> (2 * h)) & 3u) << 8);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar_tfull[h][e]);
+            }
+            if (++e == C::NTABLE) { e = 0; ++use_e; }
         }
     }
 
@@ -807,11 +780,27 @@ __global__ void __launch_bounds__(256) streamkl_stat_finish_kernel(const StatPar
         const long long total = stat_total<MODE>(p, false), run = stat_run(total, p.grid);
         const long long u = ((long long)blockIdx.x + 1) * run;
         int b = 0, hk = 0, t = 0, lo = 0;
-        if (u < total) stat_find<MODE>(p, u, b, hk, t, lo);
+        if (u < total && (int)blockIdx.x + 1 < p.grid) stat_find<MODE>(p, u, b, hk, t, lo);
         if (threadIdx.x == 0) {
             rec[0] = b; rec[1] = hk; rec[2] = t;
             rec[3] = lo > 0 && lo <= run ? u - lo : -1;       // the item's first unit
             rec[4] = run;
+        }
+    }
+    // Items without a tile (all keys of the batch element, or of the key tile, are
+    // padding): written by nobody else, so at once.
+    if (p.kv_len && !(MODE == kKeyMass && p.accumulate)) {
+        const int per = MODE == kKeyMass ? (p.N_K + 255) / 256 : TileList<MODE>(p, p.N_K).own;
+        for (long long x = blockIdx.x; x < (long long)p.B * p.Hk * per; x += gridDim.x) {
+            StatItem it;
+            it.t = (int)(x % per);
+            it.hk = (int)(x / per % p.Hk);
+            it.b = (int)(x / per / p.Hk);
+            it.nk = key_count(p.kv_len, it.b, p.N_K, p.st.word, false);
+            if (MODE == kKeyMass ? it.t * 256 < it.nk : it.nk > 0) continue;
+            int i;
+            const long long at = stat_out<MODE>(p, it, threadIdx.x, i);
+            if (at >= 0) (MODE == kKeyMass ? p.mass : p.lse)[at] = MODE == kKeyMass ? 0.f : -INFINITY;
         }
     }
     __syncthreads();
