@@ -304,7 +304,8 @@ streamkl_status streamkl_decode(const void *q, const long long *q_stride, const 
     p.mass = mass; p.mass_out = mass_out; p.mass_cap = mass_cap;
     p.grid = ds.grid;
     p.by_row = ds.by_row;
-    p.row_cost = d == 64 ? 3 : 2;
+    // (24 ragged sequences, d = 128: 59, 31, 29 and 39 us at 0, 2, 3 and 6 tiles)
+    p.row_cost = d == 64 ? 5 : 3;
     p.word = static_cast<uint32_t *>(workspace);
     cudaStream_t s = (cudaStream_t)stream;
     if (dtype == kDtypeBf16)

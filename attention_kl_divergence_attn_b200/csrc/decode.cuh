@@ -68,7 +68,7 @@ template <int D>
 struct DecCfg {
     static constexpr int ROW = D * 2;
     static constexpr int STAGE = 16 * ROW * 2;                      // K and V rows of 16 tokens
-    static constexpr int NSTAGE = D == 128 ? 3 : 6;
+    static constexpr int NSTAGE = D == 128 ? 3 : 4;
     static constexpr int RING = kDecWarps * NSTAGE * STAGE;
     static constexpr int MERGE = kDecWarps * 16 * (D + 2) * 4;      // the warps' states, after the ring is drained
     static constexpr int SMEM = RING > MERGE ? RING : MERGE;
@@ -271,30 +271,34 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) streamkl_decode_kernel(cons
         const uint32_t ring = smem_u32(smem) + warp * C::NSTAGE * C::STAGE;
         const T *kb = static_cast<const T *>(p.k.ptr) + hk * p.k.s_head;
         const T *vb = static_cast<const T *>(p.v.ptr) + hk * p.v.s_head;
-        auto page_of = [&](int tile) -> int {                    // lane t < 16: page of this warp's token t, or -1
+        // where this warp's token t of a tile lies (lane t < 16, elements from the
+        // key head's base), or -1
+        struct Place { long long k, v; };
+        const bool alike = p.k.s_page == p.v.s_page && p.k.s_slot == p.v.s_slot;
+        auto place_of = [&](int tile) -> Place {
             const int t = tile * kDecTile + warp * 16 + (lane & 15);
-            if (tile >= t1 || t >= n) return -1;
-            const int pg = __ldg(p.table + (size_t)b * p.table_b + t / p.page);
+            if (tile >= t1 || t >= n) return {-1, -1};
+            const int at = t / p.page, slot = t - at * p.page, pg = __ldg(p.table + (size_t)b * p.table_b + at);
             if ((unsigned)pg >= (unsigned)p.pages) {
                 if (p.word) atomicOr(p.word, (uint32_t)kStatusBadPage);
-                return -1;
+                return {-1, -1};
             }
-            return pg;
+            const long long k = pg * p.k.s_page + slot * p.k.s_slot;
+            return {k, alike ? k : pg * p.v.s_page + slot * p.v.s_slot};
         };
-        auto fetch = [&](int tile, int pg, int stage) {
+        auto fetch = [&](Place pl, int stage) {
             constexpr int CH = D / 8;                            // 16-byte chunks in a row
             constexpr int RPI = 32 / CH;                         // rows a warp copies at a time
             const uint32_t dst = ring + stage * C::STAGE;
+            const int ch = lane % CH;
 #pragma unroll
             for (int x = 0; x < 16 / RPI; ++x) {
-                const int r = x * RPI + lane / CH, ch = lane % CH;
-                const int row_pg = __shfl_sync(0xffffffffu, pg, r);
-                const int slot = (tile * kDecTile + warp * 16 + r) % p.page;
-                const bool ok = row_pg >= 0;
-                const size_t pgz = ok ? row_pg : 0, sl = ok ? slot : 0;
+                const int r = x * RPI + lane / CH;
+                const long long ko = __shfl_sync(0xffffffffu, pl.k, r), vo = __shfl_sync(0xffffffffu, pl.v, r);
+                const int bytes = ko >= 0 ? 16 : 0;
                 const uint32_t at = r * C::ROW + ((ch ^ (r & 7)) << 4);
-                cp_async16(dst + at, kb + pgz * p.k.s_page + sl * p.k.s_slot + ch * 8, ok ? 16 : 0);
-                cp_async16(dst + 16 * C::ROW + at, vb + pgz * p.v.s_page + sl * p.v.s_slot + ch * 8, ok ? 16 : 0);
+                cp_async16(dst + at, kb + (bytes ? ko : 0) + ch * 8, bytes);
+                cp_async16(dst + 16 * C::ROW + at, vb + (bytes ? vo : 0) + ch * 8, bytes);
             }
         };
 
@@ -304,13 +308,13 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) streamkl_decode_kernel(cons
         float M[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // rows g4 and g4 + 8
 
         uint32_t seen[C::NSTAGE];                                // which of the stage's 16 tokens exist
-        int pg_next = page_of(t0);
+        Place next = place_of(t0);
 #pragma unroll
         for (int s = 0; s < C::NSTAGE - 1; ++s) {
-            const int pg = pg_next;
-            pg_next = page_of(t0 + s + 1);
-            seen[s] = __ballot_sync(0xffffffffu, pg >= 0) & 0xffffu;
-            if (t0 + s < t1) fetch(t0 + s, pg, s);
+            const Place pl = next;
+            next = place_of(t0 + s + 1);
+            seen[s] = __ballot_sync(0xffffffffu, pl.k >= 0) & 0xffffu;
+            if (t0 + s < t1) fetch(pl, s);
             cp_commit();
         }
         for (int tb = t0; tb < t1; tb += C::NSTAGE) {
@@ -320,10 +324,11 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) streamkl_decode_kernel(cons
                 if (tile >= t1) break;
                 {   // the tile NSTAGE-1 ahead, into the stage that was read last
                     constexpr int A = C::NSTAGE - 1;
-                    const int pg = pg_next, ns = (s + A) % C::NSTAGE;
-                    pg_next = page_of(tile + A + 1);
-                    seen[ns] = __ballot_sync(0xffffffffu, pg >= 0) & 0xffffu;
-                    if (tile + A < t1) fetch(tile + A, pg, ns);
+                    const Place pl = next;
+                    const int ns = (s + A) % C::NSTAGE;
+                    next = place_of(tile + A + 1);
+                    seen[ns] = __ballot_sync(0xffffffffu, pl.k >= 0) & 0xffffu;
+                    if (tile + A < t1) fetch(pl, ns);
                     cp_commit();
                 }
                 cp_wait<C::NSTAGE - 1>();
