@@ -483,9 +483,17 @@ def _longs(s):
     return (ctypes.c_longlong * len(s))(*s)
 
 
+def _span(t):
+    """Addresses of the first byte and past the last (strides are positive here)."""
+    p = t.data_ptr()
+    if t.numel() == 0:
+        return p, p
+    return p, p + (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * t.element_size()
+
+
 def _overlap(a, b):
-    pa, pb = a.data_ptr(), b.data_ptr()
-    return pa < pb + b.numel() * b.element_size() and pb < pa + a.numel() * a.element_size()
+    (a0, a1), (b0, b1) = _span(a), _span(b)
+    return a0 < b1 and b0 < a1
 
 
 @functools.lru_cache(maxsize=4096)
@@ -535,11 +543,13 @@ def streamkl_key_mass(q, k, lse=None, scale=None, causal=False, *, kv_len=None, 
             return streamkl_key_mass(q, k, lse, scale, causal, kv_len=kv_len, out=out, accumulate=accumulate)
     word = _status_word(dev)
     mass = torch.empty(mass_shape, dtype=torch.float32, device=device) if out is None else out
+    if out is not None and any(_overlap(out, t) for t in (q, k, lse, kv_len) if t is not None):
+        raise ValueError("out must not overlap the inputs")
     given = lse is not None
     if not given:
         lse = torch.empty(row_shape, dtype=torch.float32, device=device)
     scratch = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
-    rc = lib().streamkl_key_mass(q.data_ptr(), qs, k.data_ptr(), ks, *sizes, default if scale is None else scale,
+    rc = lib().streamkl_key_mass(q.data_ptr(), qs, k.data_ptr(), ks, *sizes, default if scale is None else float(scale),
                                  1 if causal else 0, None if kv_len is None else kv_len.data_ptr(), lse.data_ptr(),
                                  given, mass.data_ptr(), 1 if accumulate else 0, word, _STATUS_BYTES,
                                  None if scratch is None else scratch.data_ptr(), nbytes, _current_stream(dev))
@@ -610,13 +620,16 @@ def streamkl_decode(q, k_pages, v_pages, page_table, seq_len, scale=None, *, mas
             if mass_out_ptr != mass_ptr and _overlap(mass, mass_out):
                 raise ValueError("mass and mass_out must be one tensor or not overlap")
     word = _status_word(dev)
+    if out is not None and any(_overlap(a, t) for a in out for t in (q, page_table, seq_len, mass, mass_out)
+                               if t is not None):
+        raise ValueError("out must not overlap the other tensors")
     if out is None:
         o, lse = torch.empty_like(q, memory_format=torch.contiguous_format), torch.empty(row_shape, dtype=torch.float32,
                                                                                         device=device)
     scratch = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
     rc = lib().streamkl_decode(q.data_ptr(), qs, k_pages.data_ptr(), ks, v_pages.data_ptr(), vs, *sizes,
                                page_table.data_ptr(), max_pages, table_stride, seq_len.data_ptr(),
-                               default if scale is None else scale, o.data_ptr(), lse.data_ptr(), mass_ptr,
+                               default if scale is None else float(scale), o.data_ptr(), lse.data_ptr(), mass_ptr,
                                mass_out_ptr, cap, word, _STATUS_BYTES,
                                None if scratch is None else scratch.data_ptr(), nbytes, _current_stream(dev))
     if rc:
@@ -677,6 +690,8 @@ def streamkl_evict(k_pages, v_pages, page_table, seq_len, mass, budget, *, recen
         with on:
             return streamkl_evict(k_pages, v_pages, page_table, seq_len, mass, budget, recent=recent, pos=pos,
                                   next_pos=next_pos, out=out)
+    if k_pages.data_ptr() == v_pages.data_ptr() and k_pages.numel():
+        raise ValueError("k_pages and v_pages must be two tensors")
     word = _status_word(dev)
     if out is None:
         new_len = torch.empty(len_shape, dtype=torch.int32, device=device)

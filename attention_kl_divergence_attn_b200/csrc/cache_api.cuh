@@ -343,6 +343,8 @@ streamkl_status streamkl_evict(void *k_pages, const long long *k_stride, void *v
     if (!cache_pointers_ok(k_pages, v_pages, num_pages, page_table, max_pages, seq_len)) return STREAMKL_ERR_INVALID_ARG;
     if ((long long)B * max_pages > 0x7fffffffll || (long long)num_pages * page_size > 0xffffffffll)
         return STREAMKL_ERR_INVALID_ARG;
+    if (paged_cap(page_size, max_pages, seq_len, mass_cap) > kEvictMaxCluster * kEvictMaxWords * 32)
+        return STREAMKL_ERR_UNSUPPORTED;
     const EvictScratch es = evict_scratch(B, H_k, num_pages, page_size, max_pages, mass_cap, budget);
     if (!scratch || scratch_bytes < es.total) return STREAMKL_ERR_WORKSPACE;
     const long long cont[3] = {(long long)H_k * page_size * d, (long long)page_size * d, d};
@@ -379,7 +381,6 @@ streamkl_status streamkl_evict(void *k_pages, const long long *k_stride, void *v
            (rows * cs <= sm_count() || p.cap / cs > kEvictMaxWords * 32))
         cs *= 2;
     p.words = ((p.cap + 31) / 32 + cs - 1) / cs;
-    if (p.words > kEvictMaxWords) return STREAMKL_ERR_UNSUPPORTED;
     if (set_smem(streamkl_evict_select_kernel, std::max(evict_smem(kEvictKeyWords), evict_smem(kEvictMaxWords))) !=
         cudaSuccess)
         return STREAMKL_ERR_CUDA;

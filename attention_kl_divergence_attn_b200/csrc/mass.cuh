@@ -238,7 +238,7 @@ __device__ __forceinline__ RowTile row_tile(const StatParams &p, int hk, int q) 
 // The row tiles that a key tile streams, in order, without a division a tile.
 struct RowCursor {
     int g, r, first;             // head of the group (packed: group of heads), tile of it, first tile that sees the keys
-    __device__ __forceinline__ RowCursor(const StatParams &p, const StatItem &it, int u) {
+    __device__ __forceinline__ void start(const StatParams &p, const StatItem &it, int u) {
         first = p.causal && !p.pack ? max(0, 2 * it.t - (p.N_K - p.N_Q + 127) / 128) : 0;
         const int per = p.pack ? 1 : p.R - first;
         g = per == 1 ? u : u / per;
@@ -480,7 +480,8 @@ __global__ void __launch_bounds__(StatCfg<D>::THREADS, 1)
                                      p.B, p.st.word);
                 }
                 ++a_asked;
-                RowCursor cur(p, it, MODE == kKeyMass ? it.lo : 0);
+                    RowCursor cur = {0, 0, 0};
+                if (MODE == kKeyMass) cur.start(p, it, it.lo);
                 for (int u = it.lo; u < it.lo + it.n; ++u, ++t) {
                     const int s = t % C::NSTAGE, n = t / C::NSTAGE;
                     ok = n == 0 || mbar_wait(&bar_empty[s], (n - 1) & 1, p.st, abort_v, 2);
@@ -722,9 +723,12 @@ __global__ void __launch_bounds__(StatCfg<D>::THREADS, 1)
 #pragma unroll
             for (int k = 0; k < 4; ++k) l[k] = in && k * 32 + lane < rt.rows ? lse[k * 32 + lane] : 0.f;
         };
-        RowCursor cur(p, iter.it, iter.it.lo);
+        RowCursor cur = {0, 0, 0};
         bool more = iter.more();
-        if (more) load_lse(cur);
+        if (more) {
+            cur.start(p, iter.it, iter.it.lo);
+            load_lse(cur);
+        }
         while (more) {
             float nb[4];
             uint32_t odd = 0u;
@@ -733,8 +737,8 @@ __global__ void __launch_bounds__(StatCfg<D>::THREADS, 1)
             for (int k = 0; k < 4; ++k) {
                 const bool in = k * 32 + lane < rows, none = fabsf(l[k]) == INFINITY;
                 nb[k] = in && !none ? -1.4426950408889634074f * l[k] : -INFINITY;
-                // (rows past a head's end are zeros, those past packed heads are not)
-                if (__any_sync(0xffffffffu, in ? none : p.pack > 0)) odd |= 1u << k;
+                // (logits of rows past the tile's end are anything: 0 times an infinite key, for instance)
+                if (__any_sync(0xffffffffu, !in || none)) odd |= 1u << k;
             }
             // the next tile's are loaded while this one's wait for their place
             if (++x < iter.it.n) {
@@ -742,7 +746,7 @@ __global__ void __launch_bounds__(StatCfg<D>::THREADS, 1)
             } else {
                 x = 0;
                 iter.next(p);
-                if ((more = iter.more())) cur = RowCursor(p, iter.it, iter.it.lo);
+                if ((more = iter.more())) cur.start(p, iter.it, iter.it.lo);
             }
             if (more) load_lse(cur);
             for (int h = 0; h < p.halves; ++h) {

@@ -381,6 +381,8 @@ size_t streamkl_evict_scratch_size(int B, int H_k, int num_pages, int page_size,
  *  - pos int32 [B,H_k,mass_cap] (position of each slot's token) and next_pos
  *    int32 [B] may be NULL when recent = 0; pos_out goes with pos.  Outputs
  *    must not overlap inputs.  0 <= recent <= budget.
+ *  - A cache with room for more than 2^21 slots a sequence is
+ *    STREAMKL_ERR_UNSUPPORTED.
  *  - A sequence that shares a page with another, or names one twice, while one
  *    of the two evicts is left as it is (new_len = its length) and reported
  *    (status word bit 4): moving rows would change the other's keys. */

@@ -85,7 +85,7 @@ def test_decode_refusals(L, kw, rc):
     (dict(budget=-1), 1), (dict(recent=-1), 1), (dict(recent=17), 1), (dict(pos=0), 1), (dict(nxt=0), 1),
     (dict(po=0), 1), (dict(pos=0, recent=0), 1), (dict(len=0), 1), (dict(new=0), 1), (dict(new=16, len=16), 1),
     (dict(mass=0), 1), (dict(mo=0), 1), (dict(mo=48), 1), (dict(po=64), 1), (dict(cap=-1), 1), (dict(sc=0), 5),
-    (dict(scb=16), 5), (dict(table=0), 1), (dict(ts=-1), 1), (dict(v=16), 1), (dict(mass=50), 1), (dict(pos=66), 1),
+    (dict(scb=16), 5), (dict(cap=1 << 22, page=1 << 16, maxp=64), 2), (dict(table=0), 1), (dict(ts=-1), 1), (dict(v=16), 1), (dict(mass=50), 1), (dict(pos=66), 1),
     (dict(ks=strides(2048, 1024, 60)), 1)])
 def test_evict_refusals(L, kw, rc):
     assert evict(L, **kw) == rc

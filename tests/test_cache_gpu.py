@@ -129,6 +129,42 @@ def test_key_mass_from_the_forward():
     assert ((total - rows).abs() <= rows * (lb[torch.isfinite(want_lse)].max() + 1e-3) * 1.01).all()
 
 
+def test_key_mass_infinite_key():
+    # a key that every row weighs with exp(-inf) received nothing
+    g = gen(18)
+    q, k = randn(g, 1, 2, 70, 64), randn(g, 1, 2, 300, 64)
+    q[..., 5] = q[..., 5].abs() + 0.5
+    k[..., 5] = k[..., 5].abs()
+    k[0, :, 33, 5] = -math.inf
+    want = ref.key_mass(q, torch.where(k.isinf(), torch.tensor(-1e4, dtype=BF), k), 0.125, False)
+    mass, lse = streamkl_key_mass(q.cuda(), k.cuda())
+    assert streamkl_check() == 0
+    assert torch.equal(mass[0, :, 33], torch.zeros_like(mass[0, :, 33]))
+    other = torch.arange(300) != 33
+    within(mass[..., other.cuda()], want[0][..., other], want[2][..., other], "mass")
+    within(lse, want[1], want[3], "lse")
+
+
+def test_overlapping_outputs_are_refused():
+    q, k = torch.randn(1, 2, 8, 64, device="cuda").to(BF), torch.randn(1, 2, 8, 64, device="cuda").to(BF)
+    lse = torch.zeros(1, 2, 8, device="cuda")
+    with pytest.raises(ValueError):
+        streamkl_key_mass(q, k, lse, out=lse)
+    t, n = torch.zeros(1, 1, dtype=torch.int32, device="cuda"), torch.full((1,), 8, dtype=torch.int32, device="cuda")
+    pages = k.clone()
+    q1 = q[:, :, 0].contiguous()
+    with pytest.raises(ValueError):
+        streamkl_decode(q1, pages, k, t, n, out=(q1, torch.empty(1, 2, device="cuda")))
+    mass = torch.zeros(3, 2, 8, device="cuda").view(-1)
+    with pytest.raises(ValueError):
+        streamkl_decode(q1, pages, k, t, n, mass=mass[:16].view(1, 2, 8), mass_out=mass[8:24].view(1, 2, 8))
+    with pytest.raises(ValueError):
+        streamkl_evict(pages, k, t, n, mass[:16].view(1, 2, 8), 4, out=(n, torch.empty(1, 2, 8, device="cuda"), None))
+    with pytest.raises(ValueError):
+        streamkl_evict(pages, pages, t, n, mass[:16].view(1, 2, 8), 4)
+    assert streamkl_check() == 0
+
+
 def test_key_mass_empty():
     q, k = torch.empty(2, 4, 0, 64, dtype=BF, device="cuda"), torch.randn(2, 2, 7, 64, device="cuda").to(BF)
     out = torch.full((2, 2, 7), math.nan, device="cuda")
