@@ -374,10 +374,11 @@ streamkl_status streamkl_evict(void *k_pages, const long long *k_stride, void *v
     p.list = es.list;
     p.word = static_cast<uint32_t *>(workspace);
     cudaStream_t s = (cudaStream_t)stream;
-    // CTAs of a cluster: twice as many as long as each keeps over 2048 slots and all run at once
+    // CTAs of a cluster: twice as many as long as each keeps over 8192 slots and all run at once
+    // (four prompts of 32 thousand slots: 60, 49 and 50 us with 2, 4 and 8)
     const long long rows = (long long)B * H_k;
     int cs = 1;
-    while (cs < kEvictMaxCluster && p.cap / cs > 2048 &&
+    while (cs < kEvictMaxCluster && p.cap / cs > 8192 &&
            (rows * cs <= sm_count() || p.cap / cs > kEvictMaxWords * 32))
         cs *= 2;
     p.words = ((p.cap + 31) / 32 + cs - 1) / cs;

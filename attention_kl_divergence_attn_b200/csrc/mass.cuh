@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(StatCfg<D>::THREADS, 1)
             mbar_init(&bar_empty[s], p.halves);
         }
         for (int s = 0; s < C::NWG; ++s) {
-            mbar_init(&bar_sfull[s], 1);
+            mbar_init(&bar_sfull[s], MODE == kKeyMass ? 2 : 1);     // the MMAs, and the issuer once it has the table
             mbar_init(&bar_sempty[s], 4);
         }
         for (int s = 0; s < C::NSLOT; ++s) {
@@ -514,14 +514,18 @@ __global__ void __launch_bounds__(StatCfg<D>::THREADS, 1)
         if (half < p.halves && elect_one()) {
             const uint64_t t0 = sw128_desc(smem_u32(sT) + half * 64 * 128, 16, 1024);
             const uint32_t id = p.fp16 ? idesc_fp16(128, 64, 0, 0) : idesc_bf16(128, 64, 0, 0);
-            int n_item = 0, s = 0, ps = 0, t = 0;
+            int n_item = 0, s = 0, ps = 0, t = 0, e = 0, pe = 0;
             bool ok = true;
             for (; ok && iter.more(); iter.next(p), ++n_item) {
                 const int a = n_item & 1;
                 if (!mbar_wait(&bar_aready[a], (n_item >> 1) & 1, p.st, abort_v, 3)) break;
                 const uint32_t ta = tmem + C::TMEM_A + a * D;
                 for (int u = 0; u < iter.it.n; ++u, ++t) {
-                    if (!(ok = mbar_wait(&bar_full[s], ps, p.st, abort_v, 4))) break;
+                    // The issuer waits for the half's table too, and its own arrival hands
+                    // the table on: a wait less in each of sixteen warps.
+                    ok = (MODE != kKeyMass || mbar_wait(&bar_tfull[half][e], pe, p.st, abort_v, 12)) &&
+                         mbar_wait(&bar_full[s], ps, p.st, abort_v, 4);
+                    if (!ok) break;
                     const uint64_t dt = desc_add(t0, s * C::TILE_BYTES);
 #pragma unroll
                     for (int m = 0; m < 2; ++m) {
@@ -533,10 +537,12 @@ __global__ void __launch_bounds__(StatCfg<D>::THREADS, 1)
                             mma_bf16_ts(tmem + buf * 64, ta + m * (D / 2) + kk * 8,
                                         desc_add(dt, (kk >> 2) * C::BOX + (kk & 3) * 32), id, kk > 0);
                         mma_commit(&bar_sfull[buf]);
+                        if (MODE == kKeyMass) mbar_arrive(&bar_sfull[buf]);
                     }
                     if (!ok) break;
                     mma_commit(&bar_empty[s]);
                     if (++s == C::NSTAGE) { s = 0; ps ^= 1; }
+                    if (++e == C::NTABLE) { e = 0; pe ^= 1; }
                 }
                 if (ok) mma_commit(&bar_aempty[a]);
             }
@@ -547,7 +553,7 @@ __global__ void __launch_bounds__(StatCfg<D>::THREADS, 1)
         const int wg = (warp - C::W_EPI) >> 2, m = wg >> 1, half = wg & 1, sub = warp & 3;
         const int lrow = sub * 32 + lane, row = m * 128 + lrow;
         const uint32_t logits = tmem + ((uint32_t)(sub * 32) << 16) + wg * 64;
-        int n_item = 0, t = 0, e = 0, pe = 0;                 // t: tiles so far; e, pe: table, its parity
+        int n_item = 0, t = 0, e = 0;                         // t: tiles so far; e: table
         bool ok = true;
         for (; ok && iter.more(); iter.next(p), ++n_item) {
             const StatItem &it = iter.it;
@@ -560,12 +566,11 @@ __global__ void __launch_bounds__(StatCfg<D>::THREADS, 1)
             const int last = MODE == kKeyMass && p.causal ? it.t * 256 + m * 128 + 127 - off : 0;
             float M = -INFINITY, l = 0.f;
             for (int x = half < p.halves ? 0 : it.n; x < it.n; ++x, ++t) {
-                if (MODE == kKeyMass) ok = warp_wait(&bar_tfull[half][e], pe, p.st, abort_v, 12);
+                ok = warp_wait(&bar_sfull[wg], t & 1, p.st, abort_v, 6);
+                if (!ok) break;
                 const int2 info = MODE == kKeyMass ? table_rows[half][e] : make_int2(0, 64);
                 const float *tab = table[half][e];
                 const int row0 = info.x, chunks = idle ? 0 : ((info.y & 255) + 31) >> 5;
-                ok = ok && warp_wait(&bar_sfull[wg], t & 1, p.st, abort_v, 6);
-                if (!ok) break;
                 tc_fence_after();
                 auto release = [&]() {                        // the logits are read
                     tc_fence_before();
@@ -630,7 +635,7 @@ __global__ void __launch_bounds__(StatCfg<D>::THREADS, 1)
                 if (MODE == kKeyMass) {
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bar_tempty[half][e]);
-                    if (++e == C::NTABLE) { e = 0; pe ^= 1; }
+                    if (++e == C::NTABLE) e = 0;
                 }
             }
             const int slot = n_item % C::NSLOT, use = n_item / C::NSLOT;
