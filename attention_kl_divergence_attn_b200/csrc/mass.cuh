@@ -434,6 +434,12 @@ __global__ void __launch_bounds__(StatCfg<D>::THREADS, 1)
         tmem_alloc(&tmem_base_sh, C::TMEM_COLS);
         tmem_relinquish();
     }
+    if (p.pack) {
+        // the rows past packed heads, which no copy fills
+        for (int x = threadIdx.x; x < (2 + C::NSTAGE) * C::TILE_BYTES / 16; x += C::THREADS)
+            reinterpret_cast<uint4 *>(sA)[x] = make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();
+    }
     if (warp == C::W_EPI) {
         // this CTA's run
         const long long total = stat_total<MODE>(p, blockIdx.x == 0), run = stat_run(total, p.grid);
@@ -557,9 +563,10 @@ __global__ void __launch_bounds__(StatCfg<D>::THREADS, 1)
         bool ok = true;
         for (; ok && iter.more(); iter.next(p), ++n_item) {
             const StatItem &it = iter.it;
-            int i, lim = 0;                                   // lim: first hidden key (rows past the tile's end see none)
+            int i;
             const bool mine = stat_out<MODE>(p, it, row, i) >= 0;
-            if (mine && MODE == kRowLse) lim = p.causal ? min(it.nk, i + off + 1) : it.nk;
+            // first hidden key (a row past the tile's end has no say in which body is taken)
+            const int lim = MODE == kRowLse && mine && p.causal ? min(it.nk, i + off + 1) : it.nk;
             const bool idle = !__any_sync(0xffffffffu, mine); // nothing of the item is this warp's
             // row i sees key j iff i >= j - off: of a head's rows, those from `first` on; `last`: the tile's largest
             const int first = MODE == kKeyMass && p.causal ? i - off : 0;
@@ -579,7 +586,7 @@ __global__ void __launch_bounds__(StatCfg<D>::THREADS, 1)
                 };
                 // two bodies: masks in the common one would cost copies of its registers
                 const int c0 = (it.lo + x) * C::BN + half * 64;              // kRowLse: the half's first key
-                const bool plain = MODE == kRowLse ? __all_sync(0xffffffffu, c0 + 64 <= lim)
+                const bool plain = MODE == kRowLse ? !idle && __all_sync(0xffffffffu, c0 + 64 <= lim)
                                                    : chunks == 2 && info.y < 256 && last <= (p.pack ? 0 : row0);
                 if (plain) {
                     // 16 columns are loaded while the 16 before them are summed
@@ -595,41 +602,55 @@ __global__ void __launch_bounds__(StatCfg<D>::THREADS, 1)
                     }
                     l += sum;         // tile by tile: a long sum's rounding grows with its number of terms
                 } else {
+                    bool masks = MODE == kRowLse || last > (p.pack ? 0 : row0);
+                    float sum = 0.f;
+                    if (!masks) {
+                        // Rows to leave out, and zero rows past the tile's end, add 2^-inf; only a key that is
+                        // not finite (or such a row) makes that NaN, and the masked sum is taken then.
+                        for (int x4 = 0; x4 < 2 * chunks; ++x4) {
+                            float u[16];
+                            tmem_ld16(logits + x4 * 16, u);
+                            tmem_ld_wait();
+                            sum += mass_chunk(u, p.c, tab + x4 * 16);
+                        }
+                        masks = __any_sync(0xffffffffu, sum != sum);
+                        if (masks) sum = 0.f;
+                    }
                     // hidden logits, and those of rows to leave out, become -inf: 2^-inf adds nothing
-                    for (int x2 = 0; x2 < chunks; ++x2) {
+                    for (int x2 = masks ? 0 : chunks; x2 < chunks; ++x2) {
+                        const int r0 = row0 + x2 * 32, h = MODE == kRowLse ? lim - c0 - x2 * 32 : first - r0;
+                        if (MODE == kRowLse ? __all_sync(0xffffffffu, h <= 0) : !p.pack && last - 127 - r0 >= 32)
+                            continue;                         // nothing seen
                         float u[32];
                         tmem_ld32(logits + x2 * 32, u);
                         tmem_ld_wait();
-                        const int r0 = row0 + x2 * 32;
-                        if (MODE == kRowLse ? __all_sync(0xffffffffu, c0 + x2 * 32 >= lim)
-                                            : !p.pack && last - 127 - r0 >= 32)
-                            continue;                         // nothing seen
-                        int h = MODE == kRowLse ? lim - c0 - x2 * 32 : first - r0;   // keys below h are seen; rows from h on see
-                        if (MODE == kKeyMass && last <= (p.pack ? 0 : r0)) {
-                            // every row sees the keys
-                        } else if (MODE == kKeyMass && p.pack) {
+                        if (MODE == kRowLse) {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                if (k >= h) u[k] = -INFINITY;
+                            lse_chunk(u, p.c, M, l);
+                            continue;
+                        }
+                        if (last > 0 && p.pack) {
                             uint32_t seen = 0u;
                             for (int k = 0; k < 32; ++k)
                                 if ((r0 + k) % p.N_Q >= first) seen |= 1u << k;
 #pragma unroll
                             for (int k = 0; k < 32; ++k)
                                 if (!((seen >> k) & 1u)) u[k] = -INFINITY;
-                        } else {
+                        } else if (last > r0 && !p.pack) {
 #pragma unroll
                             for (int k = 0; k < 32; ++k)
-                                if (MODE == kRowLse ? k >= h : k < h) u[k] = -INFINITY;
+                                if (k < h) u[k] = -INFINITY;
                         }
-                        if (MODE == kRowLse) {
-                            lse_chunk(u, p.c, M, l);
-                        } else {
-                            if ((info.y >> (8 + x2)) & 1) {
+                        if ((info.y >> (8 + x2)) & 1) {
 #pragma unroll
-                                for (int k = 0; k < 32; ++k)
-                                    if (tab[x2 * 32 + k] == -INFINITY) u[k] = -INFINITY;
-                            }
-                            l += mass_chunk(u, p.c, tab + x2 * 32);
+                            for (int k = 0; k < 32; ++k)
+                                if (tab[x2 * 32 + k] == -INFINITY) u[k] = -INFINITY;
                         }
+                        sum += mass_chunk(u, p.c, tab + x2 * 32);
                     }
+                    l += sum;
                     release();
                 }
                 if (MODE == kKeyMass) {
@@ -742,7 +763,6 @@ __global__ void __launch_bounds__(StatCfg<D>::THREADS, 1)
             for (int k = 0; k < 4; ++k) {
                 const bool in = k * 32 + lane < rows, none = fabsf(l[k]) == INFINITY;
                 nb[k] = in && !none ? -1.4426950408889634074f * l[k] : -INFINITY;
-                // (logits of rows past the tile's end are anything: 0 times an infinite key, for instance)
                 if (__any_sync(0xffffffffu, !in || none)) odd |= 1u << k;
             }
             // the next tile's are loaded while this one's wait for their place
