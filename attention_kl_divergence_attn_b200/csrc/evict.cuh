@@ -24,7 +24,8 @@
 // of the chain of dependent steps: the slots of a long sequence are spread over
 // up to 8 CTAs that add their histograms through distributed shared memory, and
 // what is kept is a bit a slot, so that ranks come from one prefix sum over the
-// words of 32 slots.
+// words of 32 slots.  Measured: 10 us for one sequence of 1040, 19 us for 32 of
+// 4160 (8 key heads), 49 us for 4 of 32768 to 4096 (selection 22, moves 27).
 #pragma once
 
 #include "decode.cuh"
@@ -357,6 +358,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) streamkl_evict_select_kernel
 // Moves the rows; nx blocks a (sequence, key head).  A sequence whose pages
 // were found shared or out of range is put back to what it was: length,
 // weights and positions copied, no row moved.
+// (More CTAs, not more rows in flight a thread: 63 us with four, 51 with one.)
 __global__ void __launch_bounds__(256, 8) streamkl_evict_move_kernel(const EvictParams p, int nx) {
     const int bk = blockIdx.x / nx, bx = blockIdx.x % nx, b = bk / p.Hk, hk = bk % p.Hk;
     grid_wait();
