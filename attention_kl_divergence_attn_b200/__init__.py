@@ -397,9 +397,12 @@ def _status_word(dev):
     if w is None:
         if torch.cuda.is_current_stream_capturing():
             raise RuntimeError("the first cache operator on a device must run before a graph capture")
-        w = torch.zeros(_STATUS_BYTES, dtype=torch.uint8, device=torch.device("cuda", dev))
-        torch.cuda.current_stream(dev).synchronize()           # cleared before any stream uses it
-        _words[dev] = w
+        with _lock:
+            w = _words.get(dev)
+            if w is None:
+                w = torch.zeros(_STATUS_BYTES, dtype=torch.uint8, device=torch.device("cuda", dev))
+                torch.cuda.current_stream(dev).synchronize()   # cleared before any stream uses it
+                _words[dev] = w
     return w.data_ptr()
 
 
@@ -418,7 +421,12 @@ def _on(dev, stream):
 
 def _sig(t):
     """What the checks of a tensor depend on (None, and what is not a tensor, stand for themselves)."""
-    return (t.dtype, t.get_device(), t.shape, t.stride()) if isinstance(t, torch.Tensor) else t
+    if t is None:
+        return None
+    try:
+        return t.dtype, t.get_device(), t.shape, t.stride()
+    except AttributeError:
+        return type(t)
 
 
 class _Meta:
@@ -479,6 +487,11 @@ def _check_pages(k_pages, v_pages, page_table, seq_len, like=None):
     return k, v, t
 
 
+def _scratch_bytes(dev, fn, *args):
+    with torch.cuda.device(dev):                               # (it depends on the device's size)
+        return int(getattr(lib(), fn)(*args))
+
+
 def _longs(s):
     return (ctypes.c_longlong * len(s))(*s)
 
@@ -516,7 +529,7 @@ def _key_mass_plan(q_sig, k_sig, lse_sig, len_sig, out_sig, accumulate):
     if out_sig is not None:
         _check_vec("out", out_sig, torch.float32, (B, H_k, N_K), dev)
     given = int(lse_sig is not None)
-    nbytes = int(lib().streamkl_key_mass_scratch_size(B, H, H_k, N_Q, N_K, d, given))
+    nbytes = _scratch_bytes(dev, "streamkl_key_mass_scratch_size", B, H, H_k, N_Q, N_K, d, given)
     return (dev, torch.device("cuda", dev), (B, H_k, N_K), (B, H, N_Q), nbytes, 1.0 / math.sqrt(max(d, 1)),
             _longs(q._stride[:3]), _longs(k._stride[:3]), (_DTYPES[q.dtype], B, H, H_k, N_Q, N_K, d))
 
@@ -582,10 +595,9 @@ def _decode_plan(q_sig, k_sig, v_sig, table_sig, len_sig, mass_sig, mass_out_sig
         _check_vec("out[0]", o_sig, q.dtype, (B, H, d), dev)
         _check_vec("out[1]", lse_sig, torch.float32, (B, H), dev)
     max_pages = table.shape[1]
-    nbytes = int(lib().streamkl_decode_scratch_size(B, H, H_k, page, max_pages, d, int(mass_sig is not None), cap))
-    return (dev, torch.device("cuda", dev), (B, H, d), (B, H), nbytes, 1.0 / math.sqrt(max(d, 1)),
-            _longs(q._stride[:2]), _longs(k._stride[:3]), _longs(v._stride[:3]),
-            (_DTYPES[q.dtype], B, H, H_k, d, pages, page), max_pages, table.stride(0), cap)
+    nbytes = _scratch_bytes(dev, "streamkl_decode_scratch_size", B, H, H_k, page, max_pages, d, int(mass_sig is not None), cap)
+    return (dev, torch.device("cuda", dev), (B, H), nbytes, 1.0 / math.sqrt(max(d, 1)), _longs(q._stride[:2]),
+            _longs(k._stride[:3]), _longs(v._stride[:3]), (_DTYPES[q.dtype], B, H, H_k, d, pages, page), max_pages, table.stride(0), cap, 4 * B * H_k * cap)
 
 
 def streamkl_decode(q, k_pages, v_pages, page_table, seq_len, scale=None, *, mass=None, mass_out=None, out=None,
@@ -604,7 +616,7 @@ def streamkl_decode(q, k_pages, v_pages, page_table, seq_len, scale=None, *, mas
     ``streamkl_check``.  Gradients do not flow.
     """
     o, lse = (None, None) if out is None else out
-    dev, device, o_shape, row_shape, nbytes, default, qs, ks, vs, sizes, max_pages, table_stride, cap = _decode_plan(
+    dev, device, row_shape, nbytes, default, qs, ks, vs, sizes, max_pages, table_stride, cap, mass_bytes = _decode_plan(
         _sig(q), _sig(k_pages), _sig(v_pages), _sig(page_table), _sig(seq_len), _sig(mass), _sig(mass_out), _sig(o),
         _sig(lse))
     on = _on(dev, stream)
@@ -617,7 +629,7 @@ def streamkl_decode(q, k_pages, v_pages, page_table, seq_len, scale=None, *, mas
         mass_ptr = mass_out_ptr = mass.data_ptr()
         if mass_out is not None:
             mass_out_ptr = mass_out.data_ptr()
-            if mass_out_ptr != mass_ptr and _overlap(mass, mass_out):
+            if mass_out_ptr != mass_ptr and abs(mass_out_ptr - mass_ptr) < mass_bytes:
                 raise ValueError("mass and mass_out must be one tensor or not overlap")
     word = _status_word(dev)
     if out is not None and any(_overlap(a, t) for a in out for t in (q, page_table, seq_len, mass, mass_out)
@@ -662,7 +674,7 @@ def _evict_plan(k_sig, v_sig, table_sig, len_sig, mass_sig, pos_sig, next_sig, o
             raise ValueError("out[2] goes with pos")
         if pos_sig is not None:
             _check_vec("out[2]", out_sigs[2], torch.int32, (B, H_k, cap), dev)
-    nbytes = int(lib().streamkl_evict_scratch_size(B, H_k, pages, page, max_pages, cap, budget))
+    nbytes = _scratch_bytes(dev, "streamkl_evict_scratch_size", B, H_k, pages, page, max_pages, cap, budget)
     return (dev, torch.device("cuda", dev), (B,), max(nbytes, 16), _longs(k._stride[:3]), _longs(v._stride[:3]),
             (B, H_k, d, pages, page), max_pages, table.stride(0), (cap, budget, recent))
 

@@ -84,7 +84,9 @@ streamkl_status launch_ex(K kern, long long grid, int threads, int smem, cudaStr
         at[c.numAttrs++].val.clusterDim.z = 1;
     }
     c.attrs = at;
-    return cudaLaunchKernelEx(&c, kern, args...) == cudaSuccess ? STREAMKL_OK : STREAMKL_ERR_CUDA;
+    if (cudaLaunchKernelEx(&c, kern, args...) == cudaSuccess) return STREAMKL_OK;
+    (void)cudaGetLastError();                        // reported here
+    return STREAMKL_ERR_CUDA;
 }
 
 template <int D, int MODE>

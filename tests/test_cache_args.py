@@ -106,6 +106,10 @@ def test_binding_refuses_cpu_tensors_and_bad_types():
         streamkl_decode(q[:, :, 0], k, k, t, n)
     with pytest.raises(TypeError):
         streamkl_evict(k, k, t, n, torch.zeros(1, 1, 4), 2)
+    with pytest.raises(TypeError):
+        streamkl_key_mass([[1.0]], k)
+    with pytest.raises(TypeError):
+        streamkl_key_mass(q.float(), k)
 
 
 # ---------------------------------------------------------- the 64-bit forms
