@@ -14,11 +14,14 @@
 // The keep-th largest is found by a radix selection, 8 bits at a time; ties at
 // that value go to the lowest slots.
 //
-// Three kernels, each started while the one before it runs:
-//   claim   every used table entry writes its number to its page's owner word
+// Kernels, each started while the one before it runs:
+//   claim   (tables of many entries) every used entry writes its number to its
+//           page's owner word
 //   select  a cluster of CTAs a (sequence, key head): selection, lists of moves,
-//           compacted weights and positions; then an entry that finds another's
-//           number in its page's owner word has met a second user of the page
+//           compacted weights and positions; then the search for pages with a
+//           second user: an entry that finds another's number in its page's owner
+//           word, or (small tables) a sequence that finds a page of its own in
+//           another's row of the table
 //   move    the rows
 // The bytes are few (8 a slot, 8 d a moved row), so what counts is the length
 // of the chain of dependent steps: the slots of a long sequence are spread over
@@ -44,6 +47,7 @@ struct EvictParams {
     int *new_len;                        // [B]
     float *mass_out;                     // [B, Hk, mass_cap]
     int *pos_out;                        // or null
+    int claims;                          // pages are claimed by a kernel of their own
     int *owner;                          // [pages]: the last claimant's sequence * max_pages + table column
     int *refused;                        // [B]: 1 = the sequence is left as it is
     int *moves;                          // [B * Hk] number of moved rows
@@ -108,12 +112,12 @@ __global__ void __launch_bounds__(kEvictThreads, 2) streamkl_evict_select_kernel
     __shared__ int2 scan_sh[2][kEvictWarps];
     __shared__ int cta_sh[3];                              // ties, holes, movers of the CTA, read by the cluster
     __shared__ uint32_t prefix_sh;
-    __shared__ int want_sh, done_sh;
+    __shared__ int want_sh, done_sh, refuse_sh;
     const int rank = cs > 1 ? (int)cluster_rank() : 0;
     const int bk = blockIdx.x / cs, b = bk / p.Hk, hk = bk % p.Hk, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
     grid_release();
-    const int n = cache_len(p.len, b, p.cap, p.word, false), keep = min(n, p.budget);
+    const int n = cache_len(p.len, b, p.cap, p.word, !p.claims && hk == 0 && tid == 0), keep = min(n, p.budget);
     const float *mass = p.mass + (size_t)bk * p.mass_cap;
     const int *pos = p.pos ? p.pos + (size_t)bk * p.mass_cap : nullptr;
     float *mass_out = p.mass_out + (size_t)bk * p.mass_cap;
@@ -334,6 +338,51 @@ __global__ void __launch_bounds__(kEvictThreads, 2) streamkl_evict_select_kernel
     grid_wait();                                           // every claim is made
     if (hk != 0) return;
     if (tid == 0 && rank == 0) p.new_len[b] = keep;
+    if (!p.claims) {
+        // A sequence with a page out of range, or that evicts or meets one that
+        // does over a common page, refuses itself (and the other does the same).
+        // A bit a page (modulo 32768) sorts out nearly all of the others' entries.
+        if (rank != 0) return;
+        const int np = (n + p.page - 1) / p.page;
+        const int *row = p.table + (size_t)b * p.table_b;
+        auto own = [&](int pg, int but) -> bool {
+            for (int y = 0; y < np; ++y)
+                if (y != but && __ldg(row + y) == pg) return true;
+            return false;
+        };
+        __syncthreads();
+        for (int x = tid; x < kEvictPasses * kEvictBins; x += kEvictThreads) hist[x] = 0;
+        if (tid == 0) refuse_sh = 0;
+        __syncthreads();
+        static_assert(kEvictPasses * kEvictBins * 32 == 32768, "bits of the histograms' memory");
+        uint32_t why = 0u;
+        for (int x = tid; x < np; x += kEvictThreads) {
+            const int pg = __ldg(row + x);
+            if ((unsigned)pg >= (unsigned)p.pages) {
+                why |= kStatusBadPage;
+                continue;
+            }
+            const int was = atomicOr(&hist[(pg & 32767) >> 5], 1 << (pg & 31));
+            if (n > keep && ((was >> (pg & 31)) & 1) && own(pg, x)) why |= kStatusSharedPage;
+        }
+        __syncthreads();
+        for (int e = tid; e < p.B * p.max_pages; e += kEvictThreads) {
+            const int ob = e / p.max_pages, x = e - ob * p.max_pages;
+            if (ob == b) continue;
+            const int on = cache_len(p.len, ob, p.cap, p.word, false);
+            if ((long long)x * p.page >= on || (n <= keep && on <= p.budget)) continue;
+            const int pg = __ldg(p.table + (size_t)ob * p.table_b + x);
+            if ((unsigned)pg < (unsigned)p.pages && ((hist[(pg & 32767) >> 5] >> (pg & 31)) & 1) && own(pg, -1))
+                why |= kStatusSharedPage;
+        }
+        if (why) {
+            if (p.word) atomicOr(p.word, why);
+            refuse_sh = 1;
+        }
+        __syncthreads();
+        if (tid == 0) p.refused[b] = refuse_sh;
+        return;
+    }
     // Of the users of a page all but the last claimant find its number: each
     // that evicts, or meets one that does, is refused, and so is that one.
     const int np = (n + p.page - 1) / p.page;

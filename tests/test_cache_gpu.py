@@ -451,7 +451,8 @@ def test_evict_long():
     assert_evicted(got, want, kc, vc)
 
 
-def test_evict_leaves_shared_and_bad_pages():
+@pytest.mark.parametrize("columns", [7, 2000])        # few entries, and more than a sequence looks through itself
+def test_evict_leaves_shared_and_bad_pages(columns):
     g = gen(12)
     lens = (100, 100, 20, 100, 64, 100, 100)
     k, v, table = cache(g, lens, 2, 64, 16, BF)
@@ -472,7 +473,9 @@ def test_evict_leaves_shared_and_bad_pages():
             budget = 49
         want = ref.evict(k, v, table.clamp(0, k.shape[0] - 1), n, mass, budget, 3, pos, nxt, skip=skip)
         kc, vc = k.cuda(), v.cuda()
-        got = streamkl_evict(kc, vc, table.cuda(), n.cuda(), mass.cuda(), budget, recent=3, pos=pos.cuda(),
+        wide = torch.full((7, columns), -9, dtype=torch.int32)
+        wide[:, :7] = table
+        got = streamkl_evict(kc, vc, wide.cuda(), n.cuda(), mass.cuda(), budget, recent=3, pos=pos.cuda(),
                              next_pos=nxt.cuda())
         with pytest.raises(StreamKLError):
             streamkl_check()
@@ -480,17 +483,40 @@ def test_evict_leaves_shared_and_bad_pages():
         assert_evicted(got, want, kc, vc)
 
 
-def test_evict_shared_prefix_without_eviction():
+@pytest.mark.parametrize("columns", [4, 5000])
+def test_evict_shared_prefix_without_eviction(columns):
     # sharing is fine while nobody evicts
     g = gen(13)
     k, v, table = cache(g, (60,), 1, 64, 16, BF)
     mass, pos, nxt = policy_inputs(g, 2, 1, 64, (60, 30))
     n = torch.tensor([60, 30], dtype=torch.int32)
     kc, vc = k.cuda(), v.cuda()
-    got = streamkl_evict(kc, vc, table.cuda().expand(2, -1), n.cuda(), mass.cuda(), 60)
+    wide = torch.zeros(1, columns, dtype=torch.int32)
+    wide[:, :4] = table
+    got = streamkl_evict(kc, vc, wide.cuda().expand(2, -1), n.cuda(), mass.cuda(), 60)
     assert streamkl_check() == 0
     assert got[0].tolist() == [60, 30]
     assert torch.equal(kc.cpu().view(torch.int16), k.view(torch.int16))
+    # and both stay as they are when one does
+    got = streamkl_evict(kc, vc, wide.cuda().expand(2, -1), n.cuda(), mass.cuda(), 40)
+    with pytest.raises(StreamKLError):
+        streamkl_check()
+    assert got[0].tolist() == [60, 30]
+    assert torch.equal(kc.cpu().view(torch.int16), k.view(torch.int16))
+
+
+def test_evict_many_columns():
+    # a table of more entries than a sequence looks through itself, used far into its rows
+    g = gen(19)
+    lens = (9000, 3, 8000)
+    k, v, table = cache(g, lens, 1, 64, 1, BF)
+    mass, pos, nxt = policy_inputs(g, 3, 1, 9000, lens)
+    n = torch.tensor(lens, dtype=torch.int32)
+    want = ref.evict(k, v, table, n, mass, 100, 10, pos, nxt)
+    kc, vc, tc, nc, mc, pc, xc = [on_gpu(x) for x in (k, v, table, n, mass, pos, nxt)]
+    got = streamkl_evict(kc, vc, tc, nc, mc, 100, recent=10, pos=pc, next_pos=xc)
+    assert streamkl_check() == 0
+    assert_evicted(got, want, kc, vc)
 
 
 # ------------------------------------------------------- streams, graphs, use
