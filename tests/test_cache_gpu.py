@@ -650,3 +650,91 @@ def test_checked_build(case):
         assert streamkl_check() == 0
     for a, b in zip(got, want):
         torch.testing.assert_close(a, b, rtol=1e-6, atol=1e-6)
+
+
+# --------------------------------------------------------------------- sweeps
+@pytest.mark.parametrize("seed", range(30))
+def test_key_mass_sweep(seed):
+    import random
+    rng = random.Random(seed)
+    Hk = rng.choice([1, 1, 2, 3])
+    G = rng.choice([1, 1, 2, 3, 7, 16, 130 if seed % 3 == 0 else 4])
+    N_K = rng.choice([1, 63, 64, 127, 128, 129, 255, 256, 257, 400, 777])
+    N_Q = rng.choice([1, 2, 5, 31, 32, 33, 60, 64, 65, 120, 128, 129, 256, 300])
+    causal = rng.random() < 0.6
+    if causal:
+        N_Q = min(N_Q, N_K)
+    if G > 16:
+        N_Q = min(N_Q, 40)
+    B, d, dtype = rng.randint(1, 4), rng.choice([64, 128]), rng.choice([BF, FP])
+    lens = None if rng.random() < 0.5 else [rng.choice([0, 1, N_K, rng.randint(0, N_K)]) for _ in range(B)]
+    g = gen(1000 + seed)
+    q, k = randn(g, B, G * Hk, N_Q, d, dtype=dtype, std=1.5), randn(g, B, Hk, N_K, d, dtype=dtype)
+    kv = None if lens is None else torch.tensor(lens, dtype=torch.int32)
+    want, want_lse, bound, lse_bound = ref.key_mass(q, k, 0.1, causal, kv)
+    out = torch.full((B, Hk, N_K), math.nan, device="cuda")
+    mass, lse = streamkl_key_mass(q.cuda(), k.cuda(), None, 0.1, causal, kv_len=None if kv is None else kv.cuda(),
+                                  out=out)
+    assert streamkl_check() == 0
+    within(mass, want, bound, "mass")
+    within(lse, want_lse, lse_bound, "lse")
+
+
+@pytest.mark.parametrize("seed", range(30))
+def test_decode_and_evict_sweep(seed):
+    import random
+    rng = random.Random(seed)
+    Hk, G = rng.choice([1, 2, 3, 8]), rng.choice([1, 2, 3, 5, 16, 17, 40])
+    page, d = rng.choice([1, 3, 16, 24, 64, 100, 256]), rng.choice([64, 128])
+    dtype, layout = rng.choice([BF, FP]), rng.choice(["HND", "NHD"])
+    top = rng.choice([1, 40, 300, 512, 513, 1500])
+    lens = [rng.choice([0, 1, rng.randint(0, top), top]) for _ in range(rng.randint(1, 6))]
+    g = gen(2000 + seed)
+    B = len(lens)
+    k, v, table = cache(g, lens, Hk, d, page, dtype, layout)
+    q = randn(g, B, G * Hk, d, dtype=dtype, std=2.0)
+    n = torch.tensor(lens, dtype=torch.int32)
+    cap = table.shape[1] * page
+    mass, pos, nxt = policy_inputs(g, B, Hk, cap, lens)
+    dev = [on_gpu(x) for x in (k, v, table, n)]
+    weight = mass.nan_to_num(0.0, 1.0, 1.0).clamp(min=0.0)
+    want = ref.decode(q, k, v, table, n, 0.12, weight)
+    wc = weight.cuda()
+    out, lse = streamkl_decode(q.cuda(), *dev, 0.12, mass=wc)
+    assert streamkl_check() == 0
+    within(out, want[0], want[3], "out")
+    within(lse, want[1], want[4], "lse")
+    within(wc, want[2], want[5], "mass")
+    budget = rng.randint(0, top + 3)
+    recent = rng.randint(0, budget)
+    want = ref.evict(k, v, table, n, mass, budget, recent, pos, nxt)
+    got = streamkl_evict(*dev, mass.cuda(), budget, recent=recent, pos=pos.cuda(), next_pos=nxt.cuda())
+    assert streamkl_check() == 0
+    assert_evicted(got, want, dev[0], dev[1])
+
+
+def test_short_caches_in_a_graph():
+    # a row a CTA and its weights in one kernel, captured and replayed on new lengths
+    g = gen(20)
+    k, v, table = cache(g, (100, 60), 2, 64, 16, BF)
+    k, v = k.nan_to_num(0.5), v.nan_to_num(0.5)
+    q = randn(g, 2, 8, 64)
+    mass = torch.rand(2, 2, 112, generator=g)
+    kc, vc, tc, qc, mc = k.cuda(), v.cuda(), table.cuda(), q.cuda(), mass.cuda()
+    n = torch.tensor([100, 60], dtype=torch.int32, device="cuda")
+    mo = torch.empty_like(mc)
+    streamkl_decode(qc, kc, vc, tc, n, mass=mc, mass_out=mo)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse = streamkl_decode(qc, kc, vc, tc, n, mass=mc, mass_out=mo)
+        new, m2, _ = streamkl_evict(kc.clone(), vc.clone(), tc, n, mo, 32)
+    for lens in ((100, 60), (7, 0), (112, 33)):
+        n.copy_(torch.tensor(lens, dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        want = ref.decode(q, k, v, table, lens, 0.125, mass)
+        within(out, want[0], want[3], "out")
+        within(lse, want[1], want[4], "lse")
+        within(mo, want[2], want[5], "mass")
+        assert new.tolist() == [min(x, 32) for x in lens]
+    assert streamkl_check() == 0
