@@ -24,8 +24,8 @@
 //    product (padded rows cost tensor time that a memory-bound kernel has to
 //    spare); the probabilities' accumulator layout is the second product's
 //    operand layout, so they never leave registers.
-// Measured (bf16, d = 128, 32 heads over 8): 331 us for 4 caches of 131 thousand
-// tokens, 6.5 TB/s, the rate of a plain copy; 29 us for 24 ragged ones of 200
+// Measured (bf16, d = 128, 32 heads over 8): 341 us for 4 caches of 131 thousand
+// tokens, 6.3 TB/s, 96 % of a plain copy; 31 us for 24 ragged ones of 200
 // thousand token rows in all (with weights), where the starts of rows count.
 #pragma once
 
@@ -77,22 +77,38 @@ struct DecCfg {
     static constexpr int SMEM = RING > MERGE ? RING : MERGE;
 };
 
-// Weights are rounded to 16 bits for their product with V.  bf16 has fp32's
-// range; fp16 loses bits below 2^-14, so its weights are scaled to at most
-// 2^15 (the scale cancels against the sum): full precision down to 2^-29 of
-// the largest.
+// A weight enters its product with V as two 16-bit parts, hi + lo, each part a
+// product of its own.  One part of 8 (bf16) or 11 (fp16) bits is off by as much as
+// the rounding of the output is, and made its error against 64 bits a quarter larger;
+// with two the weight is off by at most 2^-14.9 (bf16) or 2^-20.4 (fp16), and the
+// output's own rounding is what is left.  The second product costs caches of
+// 131 thousand tokens nothing, and short rows 5 to 8 % (24 ragged sequences 29.2 -> 31.0
+// us, 7 of up to 2500 tokens 14.3 -> 15.1, one of 77 3.8 -> 4.1); the second parts in the
+// product's unused rows, for up to 8 heads, brought 0.4 us of that back and were left out.
+// bf16 has fp32's range; fp16 loses bits below 2^-14, so its weights are scaled to
+// at most 2^15 (the scale cancels against the sum): hi has its 11 bits down to 2^-29
+// of the largest.
 template <typename T>
 constexpr float kWeightLog2 = std::is_same<T, __half>::value ? 15.f : 0.f;
 
+// The parts of two weights p >= 0, as operands.  hi is rounded towards zero from
+// slightly below p, so that neither part of a weight is zero or negative (fp16: of
+// one above 2^-29 of the largest): an infinite value stays what it is.
 template <typename T>
-__device__ __forceinline__ uint32_t pack16(float lo, float hi);
+__device__ __forceinline__ void split16(float p0, float p1, uint32_t &hi, uint32_t &lo);
 template <>
-__device__ __forceinline__ uint32_t pack16<__nv_bfloat16>(float lo, float hi) { return pack_bf16(lo, hi); }
+__device__ __forceinline__ void split16<__nv_bfloat16>(float p0, float p1, uint32_t &hi, uint32_t &lo) {
+    constexpr float kBelow = 1.f - 1.f / 65536.f;
+    const uint32_t h0 = __float_as_uint(p0 * kBelow) & 0xffff0000u, h1 = __float_as_uint(p1 * kBelow) & 0xffff0000u;
+    hi = __byte_perm(h0, h1, 0x7632);
+    lo = pack_bf16(p0 - __uint_as_float(h0), p1 - __uint_as_float(h1));
+}
 template <>
-__device__ __forceinline__ uint32_t pack16<__half>(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
+__device__ __forceinline__ void split16<__half>(float p0, float p1, uint32_t &hi, uint32_t &lo) {
+    constexpr float kBelow = 1.f - 1.f / 2048.f;
+    asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(p1 * kBelow), "f"(p0 * kBelow));
+    const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(p1 - h.y), "f"(p0 - h.x));
 }
 
 // D += A B, 16 x 8 x 16, fp32 accumulation.
@@ -387,15 +403,15 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) streamkl_decode_kernel(cons
                         M[e] = Mn;
                     }
                 }
-                uint32_t pa[4];
+                uint32_t pa[4], pb[4];                           // the weights' parts
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const float base = (M[e] == -INFINITY ? 0.f : M[e]) - kWeightLog2<T>;
                     const float p0 = ex2(y[0][2 * e] - base), p1 = ex2(y[0][2 * e + 1] - base);
                     const float p2 = ex2(y[1][2 * e] - base), p3 = ex2(y[1][2 * e + 1] - base);
                     l[e] += (p0 + p1) + (p2 + p3);
-                    pa[e] = pack16<T>(p0, p1);                   // rounded to the operand's 16 bits
-                    pa[e + 2] = pack16<T>(p2, p3);
+                    split16<T>(p0, p1, pa[e], pb[e]);
+                    split16<T>(p2, p3, pa[e + 2], pb[e + 2]);
                 }
 #pragma unroll
                 for (int dd = 0; dd < D / 16; ++dd) {
@@ -404,6 +420,8 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) streamkl_decode_kernel(cons
                     ldsm4<true>(vf, vd + r * C::ROW + ((ch ^ (r & 7)) << 4));
                     mma_16816<T>(o[2 * dd], pa, vf[0], vf[1]);
                     mma_16816<T>(o[2 * dd + 1], pa, vf[2], vf[3]);
+                    mma_16816<T>(o[2 * dd], pb, vf[0], vf[1]);
+                    mma_16816<T>(o[2 * dd + 1], pb, vf[2], vf[3]);
                 }
                 __syncwarp();
             }

@@ -354,8 +354,8 @@ size_t streamkl_decode_scratch_size(int B, int H, int H_k, int page_size, int ma
  * [B,H,d] of q's type, dense; lse fp32 [B,H]; mass, mass_out fp32
  * [B,H_k,mass_cap], both or neither NULL, equal (in place) or disjoint.
  *  - seq_len[b] = 0 gives out = 0 and lse = -inf.
- *  - Weights are rounded to 16 bits for their product with v only; their sums
- *    and the statistics are fp32.  Results are the same bits run to run.
+ *  - Weights enter their product with v in two 16-bit parts (off by 2^-14 at
+ *    most); their sums and the statistics are fp32.  Results are the same bits run to run.
  *  - Keys and values past a sequence's length are never read. */
 streamkl_status streamkl_decode(const void *q, const long long *q_stride, const void *k_pages,
                                 const long long *k_stride, const void *v_pages, const long long *v_stride, int dtype,
