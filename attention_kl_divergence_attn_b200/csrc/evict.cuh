@@ -73,11 +73,18 @@ __device__ __forceinline__ uint32_t weight_key(float m, bool recent) {
     return recent ? 0xffffffffu : (m > 0.f ? __float_as_uint(m) : 0u);
 }
 
+// Columns of the table that a sequence of n slots uses.  (A page may be as large as
+// 2^31 - 1 slots, so n + page - 1 would overflow, and no page would be looked at.)
+__host__ __device__ constexpr int used_pages(int n, int page) { return n > 0 ? (n - 1) / page + 1 : 0; }
+static_assert(used_pages(0, 1) == 0 && used_pages(1, 16) == 1 && used_pages(16, 16) == 1 && used_pages(17, 16) == 2 &&
+              used_pages(2, 0x7fffffff) == 1 && used_pages(1 << 21, 0x7fffffff) == 1 && used_pages(1 << 21, 1) == 1 << 21,
+              "no sum leaves 32 bits");
+
 __global__ void __launch_bounds__(256) streamkl_evict_claim_kernel(const EvictParams p) {
     grid_release();
     const int b = blockIdx.x;
     if (threadIdx.x == 0) p.refused[b] = 0;
-    const int n = cache_len(p.len, b, p.cap, p.word, threadIdx.x == 0), np = (n + p.page - 1) / p.page;
+    const int n = cache_len(p.len, b, p.cap, p.word, threadIdx.x == 0), np = used_pages(n, p.page);
     for (int x = threadIdx.x; x < np; x += 256) {
         const int pg = __ldg(p.table + (size_t)b * p.table_b + x);
         if ((unsigned)pg < (unsigned)p.pages) p.owner[pg] = b * p.max_pages + x;
@@ -343,7 +350,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) streamkl_evict_select_kernel
         // does over a common page, refuses itself (and the other does the same).
         // A bit a page (modulo 32768) sorts out nearly all of the others' entries.
         if (rank != 0) return;
-        const int np = (n + p.page - 1) / p.page;
+        const int np = used_pages(n, p.page);
         const int *row = p.table + (size_t)b * p.table_b;
         auto own = [&](int pg, int but) -> bool {
             for (int y = 0; y < np; ++y)
@@ -385,7 +392,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) streamkl_evict_select_kernel
     }
     // Of the users of a page all but the last claimant find its number: each
     // that evicts, or meets one that does, is refused, and so is that one.
-    const int np = (n + p.page - 1) / p.page;
+    const int np = used_pages(n, p.page);
     for (int x = rank * kEvictThreads + tid; x < np; x += cs * kEvictThreads) {
         const int pg = __ldg(p.table + (size_t)b * p.table_b + x);
         if ((unsigned)pg >= (unsigned)p.pages) {

@@ -1,0 +1,49 @@
+"""The cache operators at the ends of their documented ranges."""
+import ctypes
+
+import pytest
+import torch
+
+import attention_kl_divergence_attn_b200 as skl
+import cache_ref as ref
+from test_cache_gpu import assert_evicted, gen, policy_inputs, randn
+
+pytestmark = pytest.mark.gpu
+BF, FP = torch.bfloat16, torch.float16
+
+
+def ptr(t):
+    return None if t is None else ctypes.c_void_p(t.data_ptr())
+
+
+def longs(*s):
+    return (ctypes.c_longlong * len(s))(*s)
+
+
+@pytest.mark.parametrize("columns", [1, 2000])        # the table looked through, and pages claimed
+def test_evict_huge_page_size(columns):
+    """A contiguous cache as pages of 2^31 - 1 slots, of which few exist: bad and shared pages are still found."""
+    g = gen(200)
+    Hk, d, room, page, budget = 2, 64, 128, 2 ** 31 - 1, 40
+    lens = (100, 80, 100, 30)
+    k, v = randn(g, 2, Hk, room, d), randn(g, 2, Hk, room, d)
+    table = torch.full((4, columns), -1, dtype=torch.int32)
+    table[:, 0] = torch.tensor([1, 9, 0, 0])              # its own, none, and one page for two
+    mass, pos, nxt = policy_inputs(g, 4, Hk, room, lens)
+    n = torch.tensor(lens, dtype=torch.int32)
+    want = ref.evict(k, v, table[:, :1].clamp(0, 1), n, mass, budget, 5, pos, nxt, skip=(1, 2, 3))
+    kc, vc, tc, nc, mc, pc, xc = [x.cuda() for x in (k, v, table, n, mass, pos, nxt)]
+    new, m2, p2 = torch.empty_like(nc), torch.empty_like(mc), torch.empty_like(pc)
+    L = skl.lib()
+    size = L.streamkl_evict_scratch_size(4, Hk, 2, page, columns, room, budget)
+    word = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    scratch = torch.empty(size, dtype=torch.uint8, device="cuda")
+    strides = longs(Hk * room * d, room * d, d)
+    stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    rc = L.streamkl_evict(ptr(kc), strides, ptr(vc), strides, 4, Hk, d, 2, page, ptr(tc), columns, columns, ptr(nc),
+                          ptr(mc), ptr(pc), ptr(xc), room, budget, 5, ptr(new), ptr(m2), ptr(p2), ptr(word), 256,
+                          ptr(scratch), size, stream)
+    assert rc == 0
+    code = ctypes.c_uint(0)
+    assert L.streamkl_check(ptr(word), stream, ctypes.byref(code)) == 1 and code.value & 0xff == 0b11000
+    assert_evicted((new, m2, p2), want, kc, vc)
