@@ -166,7 +166,8 @@ streamkl_status launch_decode(const DecodeParams &p, cudaStream_t s) {
     auto kern = p.by_row ? streamkl_decode_kernel<T, D, true> : streamkl_decode_kernel<T, D, false>;
     if (set_smem(kern, DecCfg<D>::SMEM) != cudaSuccess) return STREAMKL_ERR_CUDA;
     streamkl_status st = launch_ex(kern, p.grid, kDecWarps * 32, DecCfg<D>::SMEM, s, false, 1, p);
-    const bool mass = p.logits && !(p.by_row && p.nhb == 1);
+    // (by the weights, not by the saved logits: without room for a slot there are none, and weights to copy still)
+    const bool mass = p.mass && p.mass_cap > 0 && !(p.by_row && p.nhb == 1);
     if (st != STREAMKL_OK || (p.by_row && !mass)) return st;
     const long long n_join = p.by_row ? 0 : ((long long)p.B * p.H + 3) / 4;
     const int nx = std::max(1, (p.mass_cap + kFinishTokens - 1) / kFinishTokens);
@@ -277,7 +278,11 @@ streamkl_status streamkl_decode(const void *q, const long long *q_stride, const 
     if (!workspace || workspace_bytes < kWorkspaceBytes) return STREAMKL_ERR_WORKSPACE;
     if (!aligned16(workspace) || !aligned16(scratch)) return STREAMKL_ERR_INVALID_ARG;
     if ((mass == nullptr) != (mass_out == nullptr)) return STREAMKL_ERR_INVALID_ARG;
-    if ((long long)B * H == 0) return STREAMKL_OK;
+    if ((long long)B * H == 0) {                             // nothing looks at the keys
+        if (B == 0 || mass == mass_out || mass_cap == 0) return STREAMKL_OK;
+        return cudaMemcpyAsync(mass_out, mass, (size_t)B * H_k * mass_cap * sizeof(float), cudaMemcpyDeviceToDevice,
+                               (cudaStream_t)stream) == cudaSuccess ? STREAMKL_OK : STREAMKL_ERR_CUDA;
+    }
     if (!q || !seq_len || !out || !lse || !aligned16(q) || !aligned16(out)) return STREAMKL_ERR_INVALID_ARG;
     if (!aligned4(lse) || !aligned4(mass) || !aligned4(mass_out)) return STREAMKL_ERR_INVALID_ARG;
     if (!cache_pointers_ok(k_pages, v_pages, num_pages, page_table, max_pages, seq_len)) return STREAMKL_ERR_INVALID_ARG;

@@ -475,7 +475,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) streamkl_decode_kernel(cons
             }
         }
         // one CTA had the whole group: its weights, from the logits just written
-        if (ROW && p.logits && p.nhb == 1) {
+        if (ROW && p.mass && p.nhb == 1) {
             float *l2 = so;                                      // (the fold is done)
             __syncthreads();
             if (threadIdx.x < nh) l2[threadIdx.x] = p.lse[(size_t)b * p.H + h0 + threadIdx.x] * 1.4426950408889634074f;

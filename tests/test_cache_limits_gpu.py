@@ -6,6 +6,7 @@ import torch
 
 import attention_kl_divergence_attn_b200 as skl
 import cache_ref as ref
+from attention_kl_divergence_attn_b200 import streamkl_check, streamkl_decode
 from test_cache_gpu import assert_evicted, gen, policy_inputs, randn
 
 pytestmark = pytest.mark.gpu
@@ -47,3 +48,20 @@ def test_evict_huge_page_size(columns):
     code = ctypes.c_uint(0)
     assert L.streamkl_check(ptr(word), stream, ctypes.byref(code)) == 1 and code.value & 0xff == 0b11000
     assert_evicted((new, m2, p2), want, kc, vc)
+
+
+@pytest.mark.parametrize("H,Hk", [(4, 2), (40, 2), (0, 2)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_decode_without_room(H, Hk, in_place):
+    """A table without a column: nothing to attend to, and the accumulated weights stay (or are copied) whole."""
+    g = gen(201)
+    mass = torch.rand(3, Hk, 1500, generator=g)
+    mc = mass.cuda()
+    mo = mc if in_place else torch.full_like(mc, float("nan"))
+    k = randn(g, 2, Hk, 16, 64).cuda()
+    out, lse = streamkl_decode(randn(g, 3, H, 64).cuda(), k, k, torch.zeros(3, 0, dtype=torch.int32, device="cuda"),
+                               torch.zeros(3, dtype=torch.int32, device="cuda"), 0.1, mass=mc, mass_out=mo)
+    assert streamkl_check() == 0
+    assert torch.equal(mo.cpu(), mass) and torch.equal(mc.cpu(), mass)
+    assert torch.equal(out.cpu(), torch.zeros(3, H, 64, dtype=BF))
+    assert torch.equal(lse.cpu(), torch.full((3, H), -float("inf")))
