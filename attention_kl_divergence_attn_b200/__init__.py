@@ -587,6 +587,8 @@ def _decode_plan(q_sig, k_sig, v_sig, table_sig, len_sig, mass_sig, mass_out_sig
         m = _meta(mass_sig)
         cap = m.shape[-1] if m is not None and len(m.shape) == 3 else 0
         _check_vec("mass", mass_sig, torch.float32, (B, H_k, cap), dev)
+        if cap == 0 and table.shape[1] > 0:
+            raise ValueError("mass must have a column for every slot that a sequence may use")
         if mass_out_sig is not None:
             _check_vec("mass_out", mass_out_sig, torch.float32, (B, H_k, cap), dev)
     elif mass_out_sig is not None:

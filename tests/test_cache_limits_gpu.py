@@ -65,3 +65,15 @@ def test_decode_without_room(H, Hk, in_place):
     assert torch.equal(mo.cpu(), mass) and torch.equal(mc.cpu(), mass)
     assert torch.equal(out.cpu(), torch.zeros(3, H, 64, dtype=BF))
     assert torch.equal(lse.cpu(), torch.full((3, H), -float("inf")))
+
+
+def test_decode_weights_without_a_column():
+    """Weights without a column leave no room for a slot, which is not the same as no weights: refused."""
+    k = torch.zeros(2, 1, 16, 64, dtype=BF, device="cuda")
+    q, n = k[:1, :, 0].contiguous(), torch.full((1,), 5, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        streamkl_decode(q, k, k, torch.zeros(1, 1, dtype=torch.int32, device="cuda"), n,
+                        mass=torch.empty(1, 1, 0, device="cuda"))
+    streamkl_decode(q, k, k, torch.zeros(1, 0, dtype=torch.int32, device="cuda"), n - 5,
+                    mass=torch.empty(1, 1, 0, device="cuda"))
+    assert streamkl_check() == 0
