@@ -42,6 +42,8 @@ namespace skl {
 
 enum StatMode { kRowLse = 0, kKeyMass = 1 };
 
+constexpr unsigned long long kTileBudgetNs = 20000;   // and a tile that a wait lasts over (some 15 times what one takes)
+
 struct StatParams {
     int B, H, Hk, G;             // G = H / Hk query heads per key head
     int N_Q, N_K, causal;
@@ -673,9 +675,17 @@ __global__ void __launch_bounds__(StatCfg<D>::THREADS, 1)
         // ------------------------------------------------------------ rows to tensor memory, sums out
         const int sub = warp & 3, row = sub * 32 + lane;
         const uint32_t dst = tmem + ((uint32_t)(sub * 32) << 16) + C::TMEM_A;
-        auto copy = [&](int n_item) -> bool {
+        // Two waits last as long as an item: for the next item's rows, which are asked for behind
+        // its last tile, and for its sums.  An item may have millions of tiles of one to three
+        // microseconds, so those waits' limit grows with it (the other roles' stays, and ends these too).
+        auto patient = [&](int tiles) -> DevStatus {
+            DevStatus st = p.st;
+            st.budget_ns += (unsigned long long)tiles * kTileBudgetNs;
+            return st;
+        };
+        auto copy = [&](int n_item, int tiles) -> bool {      // `tiles`: of the item before it
             const int a = n_item & 1, use = n_item >> 1;
-            if (!warp_wait(&bar_afull, n_item & 1, p.st, abort_v, 7)) return false;
+            if (!warp_wait(&bar_afull, n_item & 1, patient(tiles), abort_v, 7)) return false;
             if (use > 0 && !warp_wait(&bar_aempty[a], (use - 1) & 1, p.st, abort_v, 11)) return false;
             tc_fence_after();
 #pragma unroll 1
@@ -706,7 +716,7 @@ __global__ void __launch_bounds__(StatCfg<D>::THREADS, 1)
         // this warp's 64 rows of an item: the sums of two warpgroups
         auto write = [&](const StatItem &it, int n_item) -> bool {
             const int slot = n_item % C::NSLOT;
-            if (!warp_wait(&bar_ifull[slot], (n_item / C::NSLOT) & 1, p.st, abort_v, 10)) return false;
+            if (!warp_wait(&bar_ifull[slot], (n_item / C::NSLOT) & 1, patient(it.n), abort_v, 10)) return false;
             const bool whole = it.n == it.count;
             // an item that two runs share: this run's first item, or its last
             float *part = p.part + ((size_t)blockIdx.x * 2 + (n_item > 0 ? 1 : 0)) * 2 * C::BM;
@@ -733,11 +743,11 @@ __global__ void __launch_bounds__(StatCfg<D>::THREADS, 1)
             if (lane == 0) mbar_arrive(&bar_iempty[slot]);
             return true;
         };
-        bool ok = !iter.more() || copy(0);
+        bool ok = !iter.more() || copy(0, 0);
         for (int n_item = 0; ok && iter.more(); ++n_item) {
             const StatItem it = iter.it;
             iter.next(p);
-            ok = (!iter.more() || copy(n_item + 1)) && write(it, n_item);
+            ok = (!iter.more() || copy(n_item + 1, it.n)) && write(it, n_item);
         }
     } else if (MODE == kKeyMass) {
         // ------------------------------------------------------------ tables

@@ -6,7 +6,7 @@ import torch
 
 import attention_kl_divergence_attn_b200 as skl
 import cache_ref as ref
-from attention_kl_divergence_attn_b200 import streamkl_check, streamkl_decode
+from attention_kl_divergence_attn_b200 import streamkl_check, streamkl_decode, streamkl_key_mass
 from test_cache_gpu import assert_evicted, gen, policy_inputs, randn
 
 pytestmark = pytest.mark.gpu
@@ -77,3 +77,31 @@ def test_decode_weights_without_a_column():
     streamkl_decode(q, k, k, torch.zeros(1, 0, dtype=torch.int32, device="cuda"), n - 5,
                     mass=torch.empty(1, 1, 0, device="cuda"))
     assert streamkl_check() == 0
+
+
+def test_key_mass_item_of_millions_of_tiles():
+    """2^18 heads of 1024 rows over one key head: every 256 keys take seconds, longer than any other wait may last.
+
+    The heads are windows of one tensor of rows.  Keys of zeros receive a weight of 1 (2^0) from every row, so
+    their sums are exact: 2^28, of terms and partial sums that are multiples of 64 below 2^30.
+    """
+    if torch.cuda.mem_get_info()[0] < 8 << 30:
+        pytest.skip("needs 8 GB")
+    H, N_Q, d = 1 << 18, 1024, 64
+    N_K = 256 * torch.cuda.get_device_properties(0).multi_processor_count
+    g = gen(202)
+    rows = randn(g, H + N_Q - 1, d)
+    q = rows.cuda().as_strided((1, H, N_Q, d), (0, d, d, 1))
+    k = torch.zeros(1, 1, N_K, d, dtype=BF)
+    k[0, 0, 300, 0] = 2.0
+    lse = torch.zeros(1, H, N_Q, device="cuda")
+    mass, _ = streamkl_key_mass(q, k.cuda(), lse, 0.125)
+    assert streamkl_check() == 0
+    got = mass[0, 0].cpu()
+    zero = torch.arange(N_K) != 300
+    assert torch.equal(got[zero], torch.full((N_K - 1,), float(H * N_Q)))
+    # row r is in min(r + 1, N_Q, ...) windows
+    times = torch.minimum(torch.arange(1, H + N_Q), torch.arange(H + N_Q - 1, 0, -1)).clamp(max=N_Q).double()
+    want = float((times * torch.exp(0.125 * 2.0 * rows[:, 0].double())).sum())
+    # a sum of 64 terms a tile half, added H N_Q / 128 times: half a step each
+    assert abs(float(got[300]) - want) <= want * (2.0 ** -24 * (H * N_Q / 128 + 64) + 2.0 ** -20)
