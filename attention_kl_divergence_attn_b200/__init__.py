@@ -509,6 +509,16 @@ def _overlap(a, b):
     return a0 < b1 and b0 < a1
 
 
+def _refused(fn, rc, outs, ins, changed=()):
+    """Raises for a call that the library refused; overlaps, which it looks for, are named here.  `changed`: tensors
+    changed in place, which may lie between each other."""
+    outs, ins, changed = [[t for t in x if t is not None] for x in (outs, ins, changed)]
+    if rc == 1 and (any(_overlap(o, i) for o in outs + changed for i in ins)
+                    or any(_overlap(o, t) for n, o in enumerate(outs) for t in outs[:n] + changed)):
+        raise ValueError("outputs must not overlap inputs or each other")
+    raise StreamKLError(fn, rc)
+
+
 @functools.lru_cache(maxsize=4096)
 def _key_mass_plan(q_sig, k_sig, lse_sig, len_sig, out_sig, accumulate):
     q = _check_rows("q", q_sig, 4)
@@ -545,8 +555,9 @@ def streamkl_key_mass(q, k, lse=None, scale=None, causal=False, *, kv_len=None, 
     are at hand (lse_t of ``streamkl_fwd`` for the teacher's q and k, same
     scale, mask and lengths); otherwise they are computed and returned.
     ``causal`` and ``kv_len`` as in ``streamkl_fwd``; a row without a visible
-    key adds nothing.  ``out`` supplies mass; with ``accumulate`` the call
-    adds to it (the pieces of a long prompt).  Gradients do not flow.
+    key adds nothing.  ``out`` supplies mass and must not overlap another
+    tensor; with ``accumulate`` the call adds to it (the pieces of a long
+    prompt).  Gradients do not flow.
     """
     dev, device, mass_shape, row_shape, nbytes, default, qs, ks, sizes = _key_mass_plan(
         _sig(q), _sig(k), _sig(lse), _sig(kv_len), _sig(out), bool(accumulate))
@@ -556,8 +567,6 @@ def streamkl_key_mass(q, k, lse=None, scale=None, causal=False, *, kv_len=None, 
             return streamkl_key_mass(q, k, lse, scale, causal, kv_len=kv_len, out=out, accumulate=accumulate)
     word = _status_word(dev)
     mass = torch.empty(mass_shape, dtype=torch.float32, device=device) if out is None else out
-    if out is not None and any(_overlap(out, t) for t in (q, k, lse, kv_len) if t is not None):
-        raise ValueError("out must not overlap the inputs")
     given = lse is not None
     if not given:
         lse = torch.empty(row_shape, dtype=torch.float32, device=device)
@@ -567,12 +576,12 @@ def streamkl_key_mass(q, k, lse=None, scale=None, causal=False, *, kv_len=None, 
                                  given, mass.data_ptr(), 1 if accumulate else 0, word, _STATUS_BYTES,
                                  None if scratch is None else scratch.data_ptr(), nbytes, _current_stream(dev))
     if rc:
-        raise StreamKLError("streamkl_key_mass", rc)
+        _refused("streamkl_key_mass", rc, (mass, None if given else lse), (q, k, kv_len, lse if given else None))
     return mass, lse
 
 
 @functools.lru_cache(maxsize=4096)
-def _decode_plan(q_sig, k_sig, v_sig, table_sig, len_sig, mass_sig, mass_out_sig, o_sig, lse_sig):
+def _decode_plan(q_sig, k_sig, v_sig, table_sig, len_sig, mass_sig, mass_out_sig, outs, o_sig, lse_sig):
     q = _check_rows("q", q_sig, 3)
     k, v, table = _check_pages(k_sig, v_sig, table_sig, len_sig, q)
     dev = q.device
@@ -593,13 +602,15 @@ def _decode_plan(q_sig, k_sig, v_sig, table_sig, len_sig, mass_sig, mass_out_sig
             _check_vec("mass_out", mass_out_sig, torch.float32, (B, H_k, cap), dev)
     elif mass_out_sig is not None:
         raise ValueError("mass_out needs mass")
-    if o_sig is not None or lse_sig is not None:
+    if outs:
         _check_vec("out[0]", o_sig, q.dtype, (B, H, d), dev)
         _check_vec("out[1]", lse_sig, torch.float32, (B, H), dev)
     max_pages = table.shape[1]
-    nbytes = _scratch_bytes(dev, "streamkl_decode_scratch_size", B, H, H_k, page, max_pages, d, int(mass_sig is not None), cap)
+    nbytes = _scratch_bytes(dev, "streamkl_decode_scratch_size", B, H, H_k, page, max_pages, d,
+                            int(mass_sig is not None), cap)
     return (dev, torch.device("cuda", dev), (B, H), nbytes, 1.0 / math.sqrt(max(d, 1)), _longs(q._stride[:2]),
-            _longs(k._stride[:3]), _longs(v._stride[:3]), (_DTYPES[q.dtype], B, H, H_k, d, pages, page), max_pages, table.stride(0), cap, 4 * B * H_k * cap)
+            _longs(k._stride[:3]), _longs(v._stride[:3]), (_DTYPES[q.dtype], B, H, H_k, d, pages, page), max_pages,
+            table.stride(0), cap)
 
 
 def streamkl_decode(q, k_pages, v_pages, page_table, seq_len, scale=None, *, mass=None, mass_out=None, out=None,
@@ -614,13 +625,13 @@ def streamkl_decode(q, k_pages, v_pages, page_table, seq_len, scale=None, *, mas
     length 0 gets 0 and -inf.  ``mass`` fp32 [B, H_k, n] accumulates the
     tokens' weights, summed over each key head's query heads: in place, or
     into ``mass_out`` (mass itself then stays as it was).  ``out`` may supply
-    the (out, lse) buffers.  Bad lengths and pages are reported by
-    ``streamkl_check``.  Gradients do not flow.
+    the (out, lse) buffers; no output may overlap another tensor.  Bad lengths
+    and pages are reported by ``streamkl_check``.  Gradients do not flow.
     """
     o, lse = (None, None) if out is None else out
-    dev, device, row_shape, nbytes, default, qs, ks, vs, sizes, max_pages, table_stride, cap, mass_bytes = _decode_plan(
-        _sig(q), _sig(k_pages), _sig(v_pages), _sig(page_table), _sig(seq_len), _sig(mass), _sig(mass_out), _sig(o),
-        _sig(lse))
+    dev, device, row_shape, nbytes, default, qs, ks, vs, sizes, max_pages, table_stride, cap = _decode_plan(
+        _sig(q), _sig(k_pages), _sig(v_pages), _sig(page_table), _sig(seq_len), _sig(mass), _sig(mass_out),
+        out is not None, _sig(o), _sig(lse))
     on = _on(dev, stream)
     if on is not None:
         with on:
@@ -631,12 +642,7 @@ def streamkl_decode(q, k_pages, v_pages, page_table, seq_len, scale=None, *, mas
         mass_ptr = mass_out_ptr = mass.data_ptr()
         if mass_out is not None:
             mass_out_ptr = mass_out.data_ptr()
-            if mass_out_ptr != mass_ptr and abs(mass_out_ptr - mass_ptr) < mass_bytes:
-                raise ValueError("mass and mass_out must be one tensor or not overlap")
     word = _status_word(dev)
-    if out is not None and any(_overlap(a, t) for a in out for t in (q, page_table, seq_len, mass, mass_out)
-                               if t is not None):
-        raise ValueError("out must not overlap the other tensors")
     if out is None:
         o, lse = torch.empty_like(q, memory_format=torch.contiguous_format), torch.empty(row_shape, dtype=torch.float32,
                                                                                         device=device)
@@ -647,7 +653,8 @@ def streamkl_decode(q, k_pages, v_pages, page_table, seq_len, scale=None, *, mas
                                mass_out_ptr, cap, word, _STATUS_BYTES,
                                None if scratch is None else scratch.data_ptr(), nbytes, _current_stream(dev))
     if rc:
-        raise StreamKLError("streamkl_decode", rc)
+        _refused("streamkl_decode", rc, (o, lse, mass if mass_out is None else mass_out),
+                 (q, k_pages, v_pages, page_table, seq_len, None if mass_out_ptr == mass_ptr else mass))
     return o, lse
 
 
@@ -692,7 +699,7 @@ def streamkl_evict(k_pages, v_pages, page_table, seq_len, mass, budget, *, recen
     the largest weight, the lower slot first among equals.  Kept tokens past
     the new length move into the slots of evicted ones before it; mass and pos
     are returned in the new order (0 and -1 past new_len), as new tensors or
-    in ``out`` = (new_len, mass, pos), which must not overlap the inputs.  pos
+    in ``out`` = (new_len, mass, pos), which must not overlap another tensor.  pos
     is None if none is given.  A sequence that shares pages with another one
     is left as it is and reported by ``streamkl_check``.
     """
@@ -713,9 +720,6 @@ def streamkl_evict(k_pages, v_pages, page_table, seq_len, mass, budget, *, recen
         pos_out = None if pos is None else torch.empty_like(pos)
     else:
         new_len, mass_out, pos_out = out
-        ins = [t for t in (seq_len, mass, pos, next_pos, page_table) if t is not None]
-        if any(_overlap(o, i) for o in out if o is not None for i in ins):
-            raise ValueError("out must not overlap the inputs")
     scratch = torch.empty(nbytes, dtype=torch.uint8, device=device)
     rc = lib().streamkl_evict(k_pages.data_ptr(), ks, v_pages.data_ptr(), vs, *sizes, page_table.data_ptr(),
                               max_pages, table_stride, seq_len.data_ptr(), mass.data_ptr(),
@@ -724,7 +728,8 @@ def streamkl_evict(k_pages, v_pages, page_table, seq_len, mass, budget, *, recen
                               mass_out.data_ptr(), None if pos_out is None else pos_out.data_ptr(), word,
                               _STATUS_BYTES, scratch.data_ptr(), nbytes, _current_stream(dev))
     if rc:
-        raise StreamKLError("streamkl_evict", rc)
+        _refused("streamkl_evict", rc, (new_len, mass_out, pos_out), (page_table, seq_len, mass, pos, next_pos),
+                 (k_pages, v_pages))
     return new_len, mass_out, pos_out
 
 

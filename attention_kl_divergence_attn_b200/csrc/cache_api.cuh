@@ -21,6 +21,39 @@ bool stride_ok(const long long *s, const long long *extent) {
     return true;
 }
 
+// The bytes from a tensor's first element to its last.
+struct Span {
+    uintptr_t a, z;
+};
+Span span_of(const void *p, unsigned __int128 bytes) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    if (!p || bytes == 0) return {0, 0};
+    return {a, bytes > UINTPTR_MAX - a ? UINTPTR_MAX : a + (uintptr_t)bytes};
+}
+// 16-bit rows of d elements.  (Of a cache's pages: as many slots as a sequence may reach,
+// for a page may be declared larger than that, and than its memory.)
+Span rows_span(const void *p, const long long *s, const long long *extent, int d) {
+    unsigned __int128 n = d;
+    for (int x = 0; x < 3; ++x) {
+        if (extent[x] <= 0) return {0, 0};
+        if (extent[x] > 1) n += (unsigned __int128)(extent[x] - 1) * (unsigned long long)s[x];
+    }
+    return span_of(p, 2 * n);
+}
+Span vec_span(const void *p, long long n) { return span_of(p, 4 * (unsigned __int128)n); }
+
+// Some output overlaps an input or another output.
+bool overlapping(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+    auto meet = [](const Span &x, const Span &y) { return x.a < y.z && y.a < x.z; };
+    for (const Span *o = outs.begin(); o != outs.end(); ++o) {
+        for (const Span &i : ins)
+            if (meet(*o, i)) return true;
+        for (const Span *q = outs.begin(); q != o; ++q)
+            if (meet(*o, *q)) return true;
+    }
+    return false;
+}
+
 // 5-D map over rows of d elements in [n3][n2][n1][d] with strides (in
 // elements) s[0], s[1], s[2], as [n3][d / 64][n2][n1][64]: box of `rows` rows x
 // `heads` x `blocks` of 64 columns, 128-byte swizzle, zeros outside, so ragged
@@ -120,6 +153,11 @@ bool paged_shape_ok(int B, int H, int H_k, int num_pages, int page_size, int max
 bool cache_pointers_ok(const void *k, const void *v, int num_pages, const int *table, int max_pages, const int *len) {
     if (num_pages > 0 && max_pages > 0 && (!k || !v || !aligned16(k) || !aligned16(v))) return false;
     return (max_pages == 0 || table) && aligned4(table) && aligned4(len);
+}
+
+Span table_span(const int *table, int B, int max_pages, long long stride) {
+    return span_of(table, max_pages > 0 ? 4 * ((unsigned __int128)(B - 1) * (unsigned long long)std::max(0ll, stride) +
+                                               max_pages) : 0);
 }
 
 int paged_cap(int page_size, int max_pages, const void *mass, int mass_cap) {
@@ -239,6 +277,10 @@ streamkl_status streamkl_key_mass(const void *q, const long long *q_stride, cons
     const long long qe[3] = {B, H, N_Q}, ke[3] = {B, H_k, N_K};
     if (!stride_ok(qs, qe) || !stride_ok(ks, ke)) return STREAMKL_ERR_INVALID_ARG;
     if (!scratch || scratch_bytes < stat_bytes()) return STREAMKL_ERR_WORKSPACE;
+    const Span lse_span = vec_span(lse, n_rows), none = {0, 0};
+    if (overlapping({vec_span(mass, n_keys), lse_given ? none : lse_span},
+                    {rows_span(q, qs, qe, d), rows_span(k, ks, ke, d), vec_span(kv_len, B), lse_given ? lse_span : none}))
+        return STREAMKL_ERR_INVALID_ARG;
     streamkl_status st = check_device();
     if (st != STREAMKL_OK) return st;
 
@@ -296,6 +338,13 @@ streamkl_status streamkl_decode(const void *q, const long long *q_stride, const 
     const long long qe[3] = {1, B, H}, pe[3] = {num_pages, H_k, page_size};
     if (!stride_ok(qs, qe) || !stride_ok(ks, pe) || !stride_ok(vs, pe)) return STREAMKL_ERR_INVALID_ARG;
     if (B > 1 && table_stride < 0) return STREAMKL_ERR_INVALID_ARG;
+    const long long rows = (long long)B * H, weights = (long long)B * H_k * mass_cap;
+    const long long used[3] = {num_pages, H_k, std::min(page_size, paged_cap(page_size, max_pages, mass, mass_cap))};
+    if (overlapping({span_of(out, (unsigned __int128)rows * d * 2), vec_span(lse, rows), vec_span(mass_out, weights)},
+                    {rows_span(q, qs, qe, d), rows_span(k_pages, ks, used, d), rows_span(v_pages, vs, used, d),
+                     table_span(page_table, B, max_pages, table_stride), vec_span(seq_len, B),
+                     vec_span(mass == mass_out ? nullptr : mass, weights)}))
+        return STREAMKL_ERR_INVALID_ARG;
     streamkl_status st = check_device();
     if (st != STREAMKL_OK) return st;
 
@@ -365,6 +414,16 @@ streamkl_status streamkl_evict(void *k_pages, const long long *k_stride, void *v
     const long long pe[3] = {num_pages, H_k, page_size};
     if (!stride_ok(ks, pe) || !stride_ok(vs, pe)) return STREAMKL_ERR_INVALID_ARG;
     if (B > 1 && table_stride < 0) return STREAMKL_ERR_INVALID_ARG;
+    // (keys and values may lie between each other: pages that hold both)
+    const long long weights = (long long)B * H_k * mass_cap;
+    const long long used[3] = {num_pages, H_k, std::min(page_size, paged_cap(page_size, max_pages, seq_len, mass_cap))};
+    const Span keys = rows_span(k_pages, ks, used, d), values = rows_span(v_pages, vs, used, d);
+    const Span table = table_span(page_table, B, max_pages, table_stride), lens = vec_span(seq_len, B);
+    const Span m = vec_span(mass, weights), at = vec_span(pos, weights), next = vec_span(next_pos, B);
+    if (overlapping({vec_span(new_len, B), vec_span(mass_out, weights), vec_span(pos_out, weights)},
+                    {keys, values, table, lens, m, at, next}) ||
+        overlapping({keys}, {table, lens, m, at, next}) || overlapping({values}, {table, lens, m, at, next}))
+        return STREAMKL_ERR_INVALID_ARG;
     streamkl_status st = check_device();
     if (st != STREAMKL_OK) return st;
 

@@ -6,6 +6,8 @@
 #include <cstring>
 #include <algorithm>
 #include <atomic>
+#include <cstdint>
+#include <initializer_list>
 #include <set>
 #include <utility>
 #include <mutex>

@@ -313,6 +313,8 @@ streamkl_status streamkl_fwd_noalloc(const void *q_t, const void *k_t, const voi
  *    and a sequence that has one is not evicted from.  Either sets a bit that
  *    streamkl_check() reports as STREAMKL_ERR_INVALID_ARG (status word bit 1:
  *    length, bit 3: page, bit 4: see streamkl_evict).
+ *  - No output may overlap an input or another output, pages included
+ *    (STREAMKL_ERR_INVALID_ARG); mass_out equal to mass is in place.
  *  - Only the first 256 bytes of `workspace` (the status word) are used.
  *    `scratch` holds a call's intermediate results: calls that may overlap on
  *    the GPU (two streams, two graphs) need one each.
@@ -379,8 +381,8 @@ size_t streamkl_evict_scratch_size(int B, int H_k, int num_pages, int page_size,
  *  - k_pages, v_pages are changed in place (16-bit rows of any type); slots
  *    from new_len[b] on keep what they held.
  *  - pos int32 [B,H_k,mass_cap] (position of each slot's token) and next_pos
- *    int32 [B] may be NULL when recent = 0; pos_out goes with pos.  Outputs
- *    must not overlap inputs.  0 <= recent <= budget.
+ *    int32 [B] may be NULL when recent = 0; pos_out goes with pos.
+ *    0 <= recent <= budget.
  *  - A cache with room for more than 2^21 slots a sequence is
  *    STREAMKL_ERR_UNSUPPORTED.
  *  - A sequence that shares a page with another, or names one twice, while one
