@@ -378,6 +378,13 @@ __device__ __forceinline__ long long stat_out(const StatParams &p, const StatIte
     return row < rt.rows ? ((long long)it.b * p.H + rt.head + g) * p.N_Q + i : -1;
 }
 
+// Values of the result (sums of keys, log-sum-exps of rows), and of the partial sums.
+template <int MODE>
+__device__ __forceinline__ long long stat_values(const StatParams &p) {
+    return MODE == kKeyMass ? (long long)p.B * p.Hk * p.N_K : (long long)p.B * p.H * p.N_Q;
+}
+__device__ __forceinline__ long long part_values(const StatParams &p) { return (long long)p.grid * 2 * 2 * 256; }
+
 template <int D, int MODE>
 __global__ void __launch_bounds__(StatCfg<D>::THREADS, 1)
     streamkl_stat_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
@@ -490,7 +497,7 @@ __global__ void __launch_bounds__(StatCfg<D>::THREADS, 1)
                                      p.B, p.st.word);
                 }
                 ++a_asked;
-                    RowCursor cur = {0, 0, 0};
+                RowCursor cur = {0, 0, 0};
                 if (MODE == kKeyMass) cur.start(p, it, it.lo);
                 for (int u = it.lo; u < it.lo + it.n; ++u, ++t) {
                     const int s = t % C::NSTAGE, n = t / C::NSTAGE;
@@ -730,11 +737,10 @@ __global__ void __launch_bounds__(StatCfg<D>::THREADS, 1)
                 const long long at = stat_out<MODE>(p, it, r, i);
                 if (MODE == kKeyMass && i >= it.nk) l = 0.f;  // keys past the length received nothing
                 if (!whole) {
+                    if (!bound_ok(part + C::BM + r < p.part + part_values(p), p.st.word, kSitePart)) continue;
                     part[r] = l;
                     if (MODE == kRowLse) part[C::BM + r] = M;
-                } else if (at >= 0 && bound_ok(at < (MODE == kKeyMass ? (long long)p.B * p.Hk * p.N_K
-                                                                      : (long long)p.B * p.H * p.N_Q),
-                                               p.st.word, kSiteRowOut)) {
+                } else if (at >= 0 && bound_ok(at < stat_values<MODE>(p), p.st.word, kSiteRowOut)) {
                     if (MODE == kRowLse) p.lse[at] = lse_value(M, l);
                     else p.mass[at] = p.accumulate ? p.mass[at] + l : l;
                 }
@@ -756,8 +762,11 @@ __global__ void __launch_bounds__(StatCfg<D>::THREADS, 1)
         RowTile rt = {0, 0, 0};
         auto load_lse = [&](const RowCursor &cur) {
             rt = cur.tile(p, iter.it.hk);
-            const float *lse = p.lse + ((size_t)iter.it.b * p.H + rt.head) * p.N_Q + rt.row0;
-            const bool in = bound_ok(iter.it.b < p.B && rt.head < p.H && rt.row0 >= 0, p.st.word, kSiteConst);
+            const long long first = ((long long)iter.it.b * p.H + rt.head) * p.N_Q + rt.row0;
+            const float *lse = p.lse + first;
+            const bool in = bound_ok(iter.it.b < p.B && rt.head < p.H && rt.row0 >= 0 &&
+                                         first + rt.rows <= (long long)p.B * p.H * p.N_Q,
+                                     p.st.word, kSiteConst);
 #pragma unroll
             for (int k = 0; k < 4; ++k) l[k] = in && k * 32 + lane < rt.rows ? lse[k * 32 + lane] : 0.f;
         };
@@ -841,7 +850,8 @@ __global__ void __launch_bounds__(256) streamkl_stat_finish_kernel(const StatPar
             if (MODE == kKeyMass ? it.t * 256 < it.nk : it.nk > 0) continue;
             int i;
             const long long at = stat_out<MODE>(p, it, threadIdx.x, i);
-            if (at >= 0) (MODE == kKeyMass ? p.mass : p.lse)[at] = MODE == kKeyMass ? 0.f : -INFINITY;
+            if (at >= 0 && bound_ok(at < stat_values<MODE>(p), p.st.word, kSiteZero))
+                (MODE == kKeyMass ? p.mass : p.lse)[at] = MODE == kKeyMass ? 0.f : -INFINITY;
         }
     }
     __syncthreads();
@@ -858,12 +868,13 @@ __global__ void __launch_bounds__(256) streamkl_stat_finish_kernel(const StatPar
     for (int c = c0; c <= c1; ++c) {
         // it is the first item of a run unless it starts inside
         const float *part = p.part + ((size_t)c * 2 + (c == c0 && start > c * run ? 1 : 0)) * 2 * 256;
+        if (!bound_ok(c >= 0 && part + 256 + r < p.part + part_values(p), p.st.word, kSitePart)) continue;
         if (MODE == kRowLse) lse_join(M, sum, part[256 + r], part[r]);
         else sum += part[r];
     }
     int i;
     const long long at = stat_out<MODE>(p, it, r, i);
-    if (at < 0) return;
+    if (at < 0 || !bound_ok(at < stat_values<MODE>(p), p.st.word, kSiteRowOut)) return;
     if (MODE == kRowLse) p.lse[at] = lse_value(M, sum);
     else p.mass[at] = p.accumulate ? p.mass[at] + sum : sum;
 }
