@@ -173,7 +173,17 @@ struct DecodeScratch {
 };
 
 // Sequences of at most this many slots are not split: a CTA streams a whole
-// row, and there is no second kernel.
+// row, and there is no second kernel.  GPU time so / split, us, d = 128, 4 heads
+// over each key head, no weights, by slots and rows (sequences x key heads):
+//            1 row      8         64          256         1024
+//     128    5.3/6.9    5.3/8.7   5.4/9.0     6.7/8.2     22.3/25.8
+//     256    7.5/7.5    7.5/8.3   7.6/10.0    9.0/10.5    35.2/37.5
+//     512    10.6/7.7   10.6/8.4  10.8/11.4   13.5/19.0   54.1/54.7
+//    1024    17.1/8.4   17.1/9.0  17.2/13.7   24.6/30.1   92.8/89.2
+// (with weights the rows' sums cost more than a second kernel from 1024 rows of 256
+// slots on: 44.0/42.9, and 72.9/62.2 at 512).  The room is known on the host and rows
+// are mostly shorter, which is what the bound leans to; a launch saved is 4 us of a
+// call's host time besides.
 constexpr int kByRowCap = 512;
 
 DecodeScratch decode_scratch(int B, int H, int H_k, int page_size, int max_pages, int d, bool with_mass, int mass_cap) {
@@ -214,9 +224,11 @@ streamkl_status launch_decode(const DecodeParams &p, cudaStream_t s) {
 }
 
 // Entries of a table up to which each sequence looks for its pages in the
-// others' rows, instead of a kernel in which pages are claimed.  A call with 65
-// entries took 22.0 us so and 24.1 with claims; with 2080 entries 24.5 and 24.4,
-// with 2717 25.4 and 24.5.
+// others' rows, instead of a kernel in which pages are claimed.  GPU time so / with
+// claims, us: 65 entries 10.2/10.4, 260 11.0/11.0, 520 11.8/11.5, 1040 (4 sequences)
+// 14.1/13.3 or (16) 13.3/12.3, 2080 18.6/16.4 or 14.7/13.0.  The launch saved is 2 us
+// of a call's host time (65 entries: 22.0 us a call for 24.1), which is what a call
+// takes where this GPU time is less: up to about 1000 entries.
 constexpr int kEvictTable = 1024;
 
 struct EvictScratch {
@@ -366,8 +378,11 @@ streamkl_status streamkl_decode(const void *q, const long long *q_stride, const 
     p.mass = mass; p.mass_out = mass_out; p.mass_cap = mass_cap;
     p.grid = ds.grid;
     p.by_row = ds.by_row;
-    // (24 ragged sequences, d = 128: 59, 31, 29 and 39 us at 0, 2, 3 and 6 tiles)
-    p.row_cost = d == 64 ? 5 : 3;
+    // At 0, 2, 3, 5 and 7 tiles: 24 sequences of 1 .. 8192 with 8 key heads 46.7, 26.0, 25.6, 26.0 and
+    // 27.0 us (d = 128; 31.5, 18.4, 18.7, 19.4 and 20.2 at d = 64), 64 of 1 .. 20000 with 2 and weights 78.8,
+    // 51.0, 49.2, 48.7 and 48.4 (53.4, 34.8, 34.1, 33.8 and 34.6), 7 of 301 .. 2500 with 16 and weights 20.0,
+    // 17.6, 17.8, 18.6 and 19.9 (15.8, 14.4, 14.3, 15.2 and 15.9).
+    p.row_cost = 3;
     p.word = static_cast<uint32_t *>(workspace);
     cudaStream_t s = (cudaStream_t)stream;
     if (dtype == kDtypeBf16)
@@ -446,8 +461,9 @@ streamkl_status streamkl_evict(void *k_pages, const long long *k_stride, void *v
     p.list = es.list;
     p.word = static_cast<uint32_t *>(workspace);
     cudaStream_t s = (cudaStream_t)stream;
-    // CTAs of a cluster: twice as many as long as each keeps over 8192 slots and all run at once
-    // (four prompts of 32 thousand slots: 60, 49 and 50 us with 2, 4 and 8)
+    // CTAs of a cluster: twice as many as long as each keeps over 8192 slots and there are no more
+    // than SMs, so that up to two an SM are launched (both fit while each keeps up to 25 thousand slots);
+    // four prompts of 32 thousand slots and 8 key heads: 60, 49 and 50 us with 2, 4 and 8
     const long long rows = (long long)B * H_k;
     int cs = 1;
     while (cs < kEvictMaxCluster && p.cap / cs > 8192 &&
