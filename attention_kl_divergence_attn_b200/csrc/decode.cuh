@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) streamkl_decode_kernel(cons
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     const int r = g4 + (x & 1) * 8, col = kk * 16 + c4 * 2 + (x >> 1) * 8;
-                    qa[kk][x] = r < nh ? __ldg(reinterpret_cast<const unsigned int *>(q + r * p.q_h + col)) : 0u;
+                    qa[kk][x] = r < nh && bound_ok(b < p.B && h0 + r < p.H, p.word, kSiteResident) ? __ldg(reinterpret_cast<const unsigned int *>(q + r * p.q_h + col)) : 0u;
                 }
             }
         }
@@ -297,11 +297,14 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) streamkl_decode_kernel(cons
         auto place_of = [&](int tile) -> Place {
             const int t = tile * kDecTile + warp * 16 + (lane & 15);
             if (tile >= t1 || t >= n) return {-1, -1};
-            const int at = t / p.page, slot = t - at * p.page, pg = __ldg(p.table + (size_t)b * p.table_b + at);
+            const int at = t / p.page, slot = t - at * p.page;
+            if (!bound_ok(b < p.B && at >= 0 && at < p.max_pages, p.word, kSiteTable)) return {-1, -1};
+            const int pg = __ldg(p.table + (size_t)b * p.table_b + at);
             if ((unsigned)pg >= (unsigned)p.pages) {
                 if (p.word) atomicOr(p.word, (uint32_t)kStatusBadPage);
                 return {-1, -1};
             }
+            if (!bound_ok(hk < p.Hk && slot >= 0 && slot < p.page, p.word, kSiteSlot)) return {-1, -1};
             const long long k = pg * p.k.s_page + slot * p.k.s_slot;
             return {k, alike ? k : pg * p.v.s_page + slot * p.v.s_slot};
         };
@@ -383,7 +386,9 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) streamkl_decode_kernel(cons
                             for (int x = 0; x < 2; ++x)
 #pragma unroll
                                 for (int z = 0; z < 2; ++z)
-                                    if (t + x * 8 + c4 * 2 + z < n) dst[x * 8 + c4 * 2 + z] = y[x][e * 2 + z];
+                                    if (t + x * 8 + c4 * 2 + z < n &&
+                                        bound_ok(t + x * 8 + c4 * 2 + z < p.cap, p.word, kSitePart))
+                                        dst[x * 8 + c4 * 2 + z] = y[x][e * 2 + z];
                         }
                 }
 #pragma unroll
@@ -460,6 +465,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) streamkl_decode_kernel(cons
                 sum = fmaf(a, so[(w * 16 + r) * D + col], sum);
                 lsum = fmaf(a, sml[2 * (w * 16 + r) + 1], lsum);
             }
+            if (!bound_ok(b < p.B && h0 + r < p.H && slot < 2 * p.grid, p.word, whole ? kSiteRowOut : kSitePart)) continue;
             if (whole) {
                 const float ov = lsum == 0.f ? 0.f : sum / lsum;
                 static_cast<T *>(p.o)[((size_t)b * p.H + h0 + r) * D + col] = T(ov);
@@ -511,6 +517,10 @@ struct RowPieces {
     int start, chunk;            // first unit of the row (its start-up included)
     int c0, c1;
     __device__ __forceinline__ size_t slot(int c) const { return 2 * (size_t)c + (c * chunk >= start ? 0 : 1); }
+    // (checked build) every piece lies in a run of the grid
+    __device__ __forceinline__ bool ok(const DecodeParams &p) const {
+        return bound_ok(c0 >= 0 && c0 <= c1 && c1 < p.grid, p.word, kSitePart);
+    }
 };
 
 // A warp's sums over the sequences: all units, and those before sequence `upto`.
@@ -584,7 +594,7 @@ __global__ void __launch_bounds__(128) streamkl_decode_finish_kernel(const Decod
             if (lane == 0) p.lse[row] = -INFINITY;
             return;
         }
-        if (rp.c0 == rp.c1) return;                              // one CTA had it whole
+        if (rp.c0 == rp.c1 || !rp.ok(p)) return;                 // one CTA had it whole
         float M, l;
         join_ml(p, rp, r, M, l);
         const float bs = M == -INFINITY ? 0.f : M;
@@ -642,7 +652,7 @@ __global__ void __launch_bounds__(128) streamkl_decode_finish_kernel(const Decod
             RowPieces rp = {0, 1, 0, 0};
             if (!p.by_row) rp = row_pieces(p, total, before, nt, hk * p.nhb + hb);
             float v;
-            if (rp.c0 == rp.c1) {
+            if (rp.c0 == rp.c1 || !rp.ok(p)) {
                 v = p.lse[(size_t)b * p.H + hk * p.G + g0 + g] * 1.4426950408889634074f;
             } else {
                 float M, l;

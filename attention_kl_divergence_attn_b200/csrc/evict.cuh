@@ -86,6 +86,7 @@ __global__ void __launch_bounds__(256) streamkl_evict_claim_kernel(const EvictPa
     if (threadIdx.x == 0) p.refused[b] = 0;
     const int n = cache_len(p.len, b, p.cap, p.word, threadIdx.x == 0), np = used_pages(n, p.page);
     for (int x = threadIdx.x; x < np; x += 256) {
+        if (!bound_ok(x < p.max_pages, p.word, kSiteTable)) break;
         const int pg = __ldg(p.table + (size_t)b * p.table_b + x);
         if ((unsigned)pg < (unsigned)p.pages) p.owner[pg] = b * p.max_pages + x;
     }
@@ -161,6 +162,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) streamkl_evict_select_kernel
         for (int k = 0; k < U; ++k) {
             const int x = x0 + k * kEvictThreads, t = w0 * 32 + x;
             if (x >= slots) break;
+            if (!bound_ok(t < p.mass_cap, p.word, kSiteSlot)) break;
             mass_out[t] = t < keep ? m[k] : 0.f;
             if (pos_out) pos_out[t] = t < keep ? q[k] : -1;
             if (keep == n) continue;
@@ -322,14 +324,17 @@ __global__ void __launch_bounds__(kEvictThreads, 2) streamkl_evict_select_kernel
             if (!is_hole && !is_mover) continue;
             // the cache's row (a bad page's is never used: the sequence is refused)
             const unsigned at_page = (unsigned)t / (unsigned)p.page;
+            if (!bound_ok(at_page < (unsigned)p.max_pages && t < p.mass_cap, p.word, kSiteTable)) continue;
             const int row = (int)((unsigned)__ldg(p.table + (size_t)b * p.table_b + at_page) * (unsigned)p.page +
                                   ((unsigned)t - at_page * (unsigned)p.page));
             if (is_hole) {
                 const int x = (int)hole_sh[w] + __popc(hole & below);
+                if (!bound_ok(x >= 0 && x < p.list, p.word, kSiteList)) continue;
                 to[x] = row;
                 to_slot[x] = t;
             } else {
                 const int x = (int)mover_sh[w] + __popc(mover & below);
+                if (!bound_ok(x >= 0 && x < p.list, p.word, kSiteList)) continue;
                 from[x] = row;
                 from_slot[x] = t;
             }
@@ -337,7 +342,9 @@ __global__ void __launch_bounds__(kEvictThreads, 2) streamkl_evict_select_kernel
         if (tid == 0 && rank == 0) p.moves[bk] = n_moves;
         if (cs > 1) cluster_sync(); else __syncthreads();  // the lists are whole
         for (int x = rank * kEvictThreads + tid; x < n_moves; x += cs * kEvictThreads) {
+            if (!bound_ok(x < p.list, p.word, kSiteList)) break;
             const int t = to_slot[x], f = from_slot[x];
+            if (!bound_ok(t >= 0 && t < keep && f >= keep && f < n, p.word, kSiteSlot)) continue;
             mass_out[t] = mass[f];
             if (pos_out) pos_out[t] = pos[f];
         }
@@ -364,6 +371,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) streamkl_evict_select_kernel
         static_assert(kEvictPasses * kEvictBins * 32 == 32768, "bits of the histograms' memory");
         uint32_t why = 0u;
         for (int x = tid; x < np; x += kEvictThreads) {
+            if (!bound_ok(x < p.max_pages, p.word, kSiteTable)) break;
             const int pg = __ldg(row + x);
             if ((unsigned)pg >= (unsigned)p.pages) {
                 why |= kStatusBadPage;
@@ -394,6 +402,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) streamkl_evict_select_kernel
     // that evicts, or meets one that does, is refused, and so is that one.
     const int np = used_pages(n, p.page);
     for (int x = rank * kEvictThreads + tid; x < np; x += cs * kEvictThreads) {
+        if (!bound_ok(x < p.max_pages, p.word, kSiteTable)) break;
         const int pg = __ldg(p.table + (size_t)b * p.table_b + x);
         if ((unsigned)pg >= (unsigned)p.pages) {
             if (p.word) atomicOr(p.word, (uint32_t)kStatusBadPage);
@@ -446,6 +455,9 @@ __global__ void __launch_bounds__(256, 8) streamkl_evict_move_kernel(const Evict
         const unsigned td = t, fd = f;
         r += step;
         if (r < m) { t = to[r]; f = from[r]; }             // the next pair while this row travels
+        if (!bound_ok(r - step < p.list && td / (unsigned)p.page < (unsigned)p.pages && fd / (unsigned)p.page < (unsigned)p.pages,
+                      p.word, kSiteSlot))
+            continue;
         *reinterpret_cast<uint4 *>(row(td)) = *reinterpret_cast<const uint4 *>(row(fd));
     }
 }

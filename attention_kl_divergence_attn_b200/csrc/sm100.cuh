@@ -40,6 +40,7 @@ constexpr bool kCheckBounds = false;
 // Site ids of the checked accesses.
 enum : uint32_t {
     kSiteTma = 1, kSiteRowOut = 2, kSiteDrain = 3, kSiteResident = 4, kSiteConst = 5, kSiteZero = 6, kSitePart = 7,
+    kSiteTable = 8, kSiteSlot = 9, kSiteList = 10,
 };
 
 // true when `ok` (always in an unchecked build); otherwise records the site.
