@@ -270,234 +270,238 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) streamkl_decode_kernel(cons
         const int h0 = hk * p.G + hb * 16, nh = min(16, p.G - hb * 16);
 
         if (ROW || t0 < t1) {                                    // (else the run ends inside the start-up)
-        // the group's query heads as the product's 16 rows (rows past nh are zero)
-        uint32_t qa[D / 16][4];
-        {
-            const T *q = static_cast<const T *>(p.q) + (size_t)b * p.q_b + (size_t)h0 * p.q_h;
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const int r = g4 + (x & 1) * 8, col = kk * 16 + c4 * 2 + (x >> 1) * 8;
-                    qa[kk][x] = r < nh && bound_ok(b < p.B && h0 + r < p.H, p.word, kSiteResident) ? __ldg(reinterpret_cast<const unsigned int *>(q + r * p.q_h + col)) : 0u;
-                }
-            }
-        }
-
-        // copies 16 tokens' K and V rows into a stage of this warp's ring; the
-        // 16-byte chunks of a row are permuted by the row so that eight rows of
-        // a column fall into different banks
-        const uint32_t ring = smem_u32(smem) + warp * C::NSTAGE * C::STAGE;
-        const T *kb = static_cast<const T *>(p.k.ptr) + hk * p.k.s_head;
-        const T *vb = static_cast<const T *>(p.v.ptr) + hk * p.v.s_head;
-        // where this warp's token t of a tile lies (lane t < 16, elements from the
-        // key head's base), or -1
-        struct Place { long long k, v; };
-        const bool alike = p.k.s_page == p.v.s_page && p.k.s_slot == p.v.s_slot;
-        auto place_of = [&](int tile) -> Place {
-            const int t = tile * kDecTile + warp * 16 + (lane & 15);
-            if (tile >= t1 || t >= n) return {-1, -1};
-            const int at = t / p.page, slot = t - at * p.page;
-            if (!bound_ok(b < p.B && at >= 0 && at < p.max_pages, p.word, kSiteTable)) return {-1, -1};
-            const int pg = __ldg(p.table + (size_t)b * p.table_b + at);
-            if ((unsigned)pg >= (unsigned)p.pages) {
-                if (p.word) atomicOr(p.word, (uint32_t)kStatusBadPage);
-                return {-1, -1};
-            }
-            if (!bound_ok(hk < p.Hk && slot >= 0 && slot < p.page, p.word, kSiteSlot)) return {-1, -1};
-            const long long k = pg * p.k.s_page + slot * p.k.s_slot;
-            return {k, alike ? k : pg * p.v.s_page + slot * p.v.s_slot};
-        };
-        auto fetch = [&](Place pl, int stage) {
-            constexpr int CH = D / 8;                            // 16-byte chunks in a row
-            constexpr int RPI = 32 / CH;                         // rows a warp copies at a time
-            const uint32_t dst = ring + stage * C::STAGE;
-            const int ch = lane % CH;
-#pragma unroll
-            for (int x = 0; x < 16 / RPI; ++x) {
-                const int r = x * RPI + lane / CH;
-                const long long ko = __shfl_sync(0xffffffffu, pl.k, r), vo = __shfl_sync(0xffffffffu, pl.v, r);
-                const int bytes = ko >= 0 ? 16 : 0;
-                const uint32_t at = r * C::ROW + ((ch ^ (r & 7)) << 4);
-                cp_async16(dst + at, kb + (bytes ? ko : 0) + ch * 8, bytes);
-                cp_async16(dst + 16 * C::ROW + at, vb + (bytes ? vo : 0) + ch * 8, bytes);
-            }
-        };
-
-        float o[D / 8][4];
-#pragma unroll
-        for (int x = 0; x < D / 8; ++x) o[x][0] = o[x][1] = o[x][2] = o[x][3] = 0.f;
-        float M[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // rows g4 and g4 + 8
-
-        uint32_t seen[C::NSTAGE];                                // which of the stage's 16 tokens exist
-        Place next = place_of(t0);
-#pragma unroll
-        for (int s = 0; s < C::NSTAGE - 1; ++s) {
-            const Place pl = next;
-            next = place_of(t0 + s + 1);
-            seen[s] = __ballot_sync(0xffffffffu, pl.k >= 0) & 0xffffu;
-            if (t0 + s < t1) fetch(pl, s);
-            cp_commit();
-        }
-        for (int tb = t0; tb < t1; tb += C::NSTAGE) {
-#pragma unroll
-            for (int s = 0; s < C::NSTAGE; ++s) {
-                const int tile = tb + s;
-                if (tile >= t1) break;
-                {   // the tile NSTAGE-1 ahead, into the stage that was read last
-                    constexpr int A = C::NSTAGE - 1;
-                    const Place pl = next;
-                    const int ns = (s + A) % C::NSTAGE;
-                    next = place_of(tile + A + 1);
-                    seen[ns] = __ballot_sync(0xffffffffu, pl.k >= 0) & 0xffffu;
-                    if (tile + A < t1) fetch(pl, ns);
-                    cp_commit();
-                }
-                cp_wait<C::NSTAGE - 1>();
-                __syncwarp();
-                const uint32_t kd = ring + s * C::STAGE, vd = kd + 16 * C::ROW;
-                // logits of 16 heads x 16 tokens
-                float y[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+            // the group's query heads as the product's 16 rows (rows past nh are zero)
+            uint32_t qa[D / 16][4];
+            {
+                const T *q = static_cast<const T *>(p.q) + (size_t)b * p.q_b + (size_t)h0 * p.q_h;
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
-                    const int r = (lane & 7) + ((lane >> 4) << 3), ch = kk * 2 + ((lane >> 3) & 1);
-                    uint32_t kf[4];
-                    ldsm4<false>(kf, kd + r * C::ROW + ((ch ^ (r & 7)) << 4));
-                    mma_16816<T>(y[0], qa[kk], kf[0], kf[1]);
-                    mma_16816<T>(y[1], qa[kk], kf[2], kf[3]);
-                }
-                const uint32_t live = seen[s];
-                float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                for (int x = 0; x < 2; ++x)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int tok = x * 8 + c4 * 2 + (e & 1);
-                        y[x][e] = (live >> tok) & 1 ? y[x][e] * p.c : -INFINITY;
-                        mx[e >> 1] = fmaxf(mx[e >> 1], y[x][e]);
+                    for (int x = 0; x < 4; ++x) {
+                        const int r = g4 + (x & 1) * 8, col = kk * 16 + c4 * 2 + (x >> 1) * 8;
+                        const bool in = r < nh && bound_ok(b < p.B && h0 + r < p.H, p.word, kSiteResident);
+                        qa[kk][x] = in ? __ldg(reinterpret_cast<const unsigned int *>(q + r * p.q_h + col)) : 0u;
                     }
-                if (p.logits) {
-                    const int t = tile * kDecTile + warp * 16;
+                }
+            }
+
+            // copies 16 tokens' K and V rows into a stage of this warp's ring; the
+            // 16-byte chunks of a row are permuted by the row so that eight rows of
+            // a column fall into different banks
+            const uint32_t ring = smem_u32(smem) + warp * C::NSTAGE * C::STAGE;
+            const T *kb = static_cast<const T *>(p.k.ptr) + hk * p.k.s_head;
+            const T *vb = static_cast<const T *>(p.v.ptr) + hk * p.v.s_head;
+            // where this warp's token t of a tile lies (lane t < 16, elements from the
+            // key head's base), or -1
+            struct Place { long long k, v; };
+            const bool alike = p.k.s_page == p.v.s_page && p.k.s_slot == p.v.s_slot;
+            auto place_of = [&](int tile) -> Place {
+                const int t = tile * kDecTile + warp * 16 + (lane & 15);
+                if (tile >= t1 || t >= n) return {-1, -1};
+                const int at = t / p.page, slot = t - at * p.page;
+                if (!bound_ok(b < p.B && at >= 0 && at < p.max_pages, p.word, kSiteTable)) return {-1, -1};
+                const int pg = __ldg(p.table + (size_t)b * p.table_b + at);
+                if ((unsigned)pg >= (unsigned)p.pages) {
+                    if (p.word) atomicOr(p.word, (uint32_t)kStatusBadPage);
+                    return {-1, -1};
+                }
+                if (!bound_ok(hk < p.Hk && slot >= 0 && slot < p.page, p.word, kSiteSlot)) return {-1, -1};
+                const long long k = pg * p.k.s_page + slot * p.k.s_slot;
+                return {k, alike ? k : pg * p.v.s_page + slot * p.v.s_slot};
+            };
+            auto fetch = [&](Place pl, int stage) {
+                constexpr int CH = D / 8;                            // 16-byte chunks in a row
+                constexpr int RPI = 32 / CH;                         // rows a warp copies at a time
+                const uint32_t dst = ring + stage * C::STAGE;
+                const int ch = lane % CH;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        if (g4 + e * 8 < nh) {
-                            float *dst = p.logits + ((size_t)b * p.H + h0 + g4 + e * 8) * p.cap + t;
+                for (int x = 0; x < 16 / RPI; ++x) {
+                    const int r = x * RPI + lane / CH;
+                    const long long ko = __shfl_sync(0xffffffffu, pl.k, r), vo = __shfl_sync(0xffffffffu, pl.v, r);
+                    const int bytes = ko >= 0 ? 16 : 0;
+                    const uint32_t at = r * C::ROW + ((ch ^ (r & 7)) << 4);
+                    cp_async16(dst + at, kb + (bytes ? ko : 0) + ch * 8, bytes);
+                    cp_async16(dst + 16 * C::ROW + at, vb + (bytes ? vo : 0) + ch * 8, bytes);
+                }
+            };
+
+            float o[D / 8][4];
 #pragma unroll
-                            for (int x = 0; x < 2; ++x)
+            for (int x = 0; x < D / 8; ++x) o[x][0] = o[x][1] = o[x][2] = o[x][3] = 0.f;
+            float M[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // rows g4 and g4 + 8
+
+            uint32_t seen[C::NSTAGE];                                // which of the stage's 16 tokens exist
+            Place next = place_of(t0);
 #pragma unroll
-                                for (int z = 0; z < 2; ++z)
-                                    if (t + x * 8 + c4 * 2 + z < n &&
-                                        bound_ok(t + x * 8 + c4 * 2 + z < p.cap, p.word, kSitePart))
-                                        dst[x * 8 + c4 * 2 + z] = y[x][e * 2 + z];
+            for (int s = 0; s < C::NSTAGE - 1; ++s) {
+                const Place pl = next;
+                next = place_of(t0 + s + 1);
+                seen[s] = __ballot_sync(0xffffffffu, pl.k >= 0) & 0xffffu;
+                if (t0 + s < t1) fetch(pl, s);
+                cp_commit();
+            }
+            for (int tb = t0; tb < t1; tb += C::NSTAGE) {
+#pragma unroll
+                for (int s = 0; s < C::NSTAGE; ++s) {
+                    const int tile = tb + s;
+                    if (tile >= t1) break;
+                    {   // the tile NSTAGE-1 ahead, into the stage that was read last
+                        constexpr int A = C::NSTAGE - 1;
+                        const Place pl = next;
+                        const int ns = (s + A) % C::NSTAGE;
+                        next = place_of(tile + A + 1);
+                        seen[ns] = __ballot_sync(0xffffffffu, pl.k >= 0) & 0xffffu;
+                        if (tile + A < t1) fetch(pl, ns);
+                        cp_commit();
+                    }
+                    cp_wait<C::NSTAGE - 1>();
+                    __syncwarp();
+                    const uint32_t kd = ring + s * C::STAGE, vd = kd + 16 * C::ROW;
+                    // logits of 16 heads x 16 tokens
+                    float y[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const int r = (lane & 7) + ((lane >> 4) << 3), ch = kk * 2 + ((lane >> 3) & 1);
+                        uint32_t kf[4];
+                        ldsm4<false>(kf, kd + r * C::ROW + ((ch ^ (r & 7)) << 4));
+                        mma_16816<T>(y[0], qa[kk], kf[0], kf[1]);
+                        mma_16816<T>(y[1], qa[kk], kf[2], kf[3]);
+                    }
+                    const uint32_t live = seen[s];
+                    float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int tok = x * 8 + c4 * 2 + (e & 1);
+                            y[x][e] = (live >> tok) & 1 ? y[x][e] * p.c : -INFINITY;
+                            mx[e >> 1] = fmaxf(mx[e >> 1], y[x][e]);
                         }
-                }
+                    if (p.logits) {
+                        const int t = tile * kDecTile + warp * 16;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
-                    mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
-                }
-                const bool up = mx[0] > M[0] || mx[1] > M[1];
-                if (__any_sync(0xffffffffu, up)) {
+                        for (int e = 0; e < 2; ++e)
+                            if (g4 + e * 8 < nh) {
+                                float *dst = p.logits + ((size_t)b * p.H + h0 + g4 + e * 8) * p.cap + t;
+#pragma unroll
+                                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                                    for (int z = 0; z < 2; ++z)
+                                        if (t + x * 8 + c4 * 2 + z < n &&
+                                            bound_ok(t + x * 8 + c4 * 2 + z < p.cap, p.word, kSitePart))
+                                            dst[x * 8 + c4 * 2 + z] = y[x][e * 2 + z];
+                            }
+                    }
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float Mn = fmaxf(M[e], mx[e]);
-                        const float a = M[e] == -INFINITY ? 0.f : ex2(M[e] - Mn);
-                        l[e] *= a;
+                        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
+                        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
+                    }
+                    const bool up = mx[0] > M[0] || mx[1] > M[1];
+                    if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
-                        for (int x = 0; x < D / 8; ++x) { o[x][2 * e] *= a; o[x][2 * e + 1] *= a; }
-                        M[e] = Mn;
+                        for (int e = 0; e < 2; ++e) {
+                            const float Mn = fmaxf(M[e], mx[e]);
+                            const float a = M[e] == -INFINITY ? 0.f : ex2(M[e] - Mn);
+                            l[e] *= a;
+#pragma unroll
+                            for (int x = 0; x < D / 8; ++x) { o[x][2 * e] *= a; o[x][2 * e + 1] *= a; }
+                            M[e] = Mn;
+                        }
+                    }
+                    uint32_t pa[4], pb[4];                           // the weights' parts
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float base = (M[e] == -INFINITY ? 0.f : M[e]) - kWeightLog2<T>;
+                        const float p0 = ex2(y[0][2 * e] - base), p1 = ex2(y[0][2 * e + 1] - base);
+                        const float p2 = ex2(y[1][2 * e] - base), p3 = ex2(y[1][2 * e + 1] - base);
+                        l[e] += (p0 + p1) + (p2 + p3);
+                        split16<T>(p0, p1, pa[e], pb[e]);
+                        split16<T>(p2, p3, pa[e + 2], pb[e + 2]);
+                    }
+#pragma unroll
+                    for (int dd = 0; dd < D / 16; ++dd) {
+                        const int r = (lane & 7) + (((lane >> 3) & 1) << 3), ch = dd * 2 + (lane >> 4);
+                        uint32_t vf[4];
+                        ldsm4<true>(vf, vd + r * C::ROW + ((ch ^ (r & 7)) << 4));
+                        mma_16816<T>(o[2 * dd], pa, vf[0], vf[1]);
+                        mma_16816<T>(o[2 * dd + 1], pa, vf[2], vf[3]);
+                        mma_16816<T>(o[2 * dd], pb, vf[0], vf[1]);
+                        mma_16816<T>(o[2 * dd + 1], pb, vf[2], vf[3]);
+                    }
+                    __syncwarp();
+                }
+            }
+            cp_wait<0>();
+            __syncthreads();
+
+            // fold the four warps' states
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+                l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+            }
+            float *so = reinterpret_cast<float *>(smem), *sml = so + kDecWarps * 16 * D;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = warp * 16 + g4 + e * 8;
+#pragma unroll
+                for (int x = 0; x < D / 8; ++x)
+                    *reinterpret_cast<float2 *>(so + r * D + x * 8 + c4 * 2) =
+                        make_float2(o[x][2 * e], o[x][2 * e + 1]);
+                if (c4 == 0) { sml[2 * r] = M[e] - kWeightLog2<T>; sml[2 * r + 1] = l[e]; }
+            }
+            __syncthreads();
+            const bool whole = t0 == 0 && t1 == nt;
+            const int slot = 2 * blockIdx.x + (u == u_first ? 0 : 1);
+            for (int x = threadIdx.x; x < nh * D; x += kDecWarps * 32) {
+                const int r = x / D, col = x % D;
+                float Mx = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < kDecWarps; ++w) Mx = fmaxf(Mx, sml[2 * (w * 16 + r)]);
+                const float bs = Mx == -INFINITY ? 0.f : Mx;
+                float sum = 0.f, lsum = 0.f;
+#pragma unroll
+                for (int w = 0; w < kDecWarps; ++w) {
+                    const float a = ex2(sml[2 * (w * 16 + r)] - bs);
+                    sum = fmaf(a, so[(w * 16 + r) * D + col], sum);
+                    lsum = fmaf(a, sml[2 * (w * 16 + r) + 1], lsum);
+                }
+                if (!bound_ok(b < p.B && h0 + r < p.H && slot < 2 * p.grid, p.word, whole ? kSiteRowOut : kSitePart))
+                    continue;
+                if (whole) {
+                    const float ov = lsum == 0.f ? 0.f : sum / lsum;
+                    static_cast<T *>(p.o)[((size_t)b * p.H + h0 + r) * D + col] = T(ov);
+                    if (col == 0)
+                        p.lse[(size_t)b * p.H + h0 + r] =
+                            lsum == 0.f ? -INFINITY : 0.69314718055994530942f * (bs + lg2(lsum));
+                } else {
+                    p.part_o[((size_t)slot * 16 + r) * D + col] = sum;
+                    if (col == 0) {
+                        p.part_ml[((size_t)slot * 16 + r) * 2] = Mx;
+                        p.part_ml[((size_t)slot * 16 + r) * 2 + 1] = lsum;
                     }
                 }
-                uint32_t pa[4], pb[4];                           // the weights' parts
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float base = (M[e] == -INFINITY ? 0.f : M[e]) - kWeightLog2<T>;
-                    const float p0 = ex2(y[0][2 * e] - base), p1 = ex2(y[0][2 * e + 1] - base);
-                    const float p2 = ex2(y[1][2 * e] - base), p3 = ex2(y[1][2 * e + 1] - base);
-                    l[e] += (p0 + p1) + (p2 + p3);
-                    split16<T>(p0, p1, pa[e], pb[e]);
-                    split16<T>(p2, p3, pa[e + 2], pb[e + 2]);
-                }
-#pragma unroll
-                for (int dd = 0; dd < D / 16; ++dd) {
-                    const int r = (lane & 7) + (((lane >> 3) & 1) << 3), ch = dd * 2 + (lane >> 4);
-                    uint32_t vf[4];
-                    ldsm4<true>(vf, vd + r * C::ROW + ((ch ^ (r & 7)) << 4));
-                    mma_16816<T>(o[2 * dd], pa, vf[0], vf[1]);
-                    mma_16816<T>(o[2 * dd + 1], pa, vf[2], vf[3]);
-                    mma_16816<T>(o[2 * dd], pb, vf[0], vf[1]);
-                    mma_16816<T>(o[2 * dd + 1], pb, vf[2], vf[3]);
-                }
-                __syncwarp();
             }
-        }
-        cp_wait<0>();
-        __syncthreads();
-
-        // fold the four warps' states
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
-            l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
-        }
-        float *so = reinterpret_cast<float *>(smem), *sml = so + kDecWarps * 16 * D;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int r = warp * 16 + g4 + e * 8;
-#pragma unroll
-            for (int x = 0; x < D / 8; ++x)
-                *reinterpret_cast<float2 *>(so + r * D + x * 8 + c4 * 2) = make_float2(o[x][2 * e], o[x][2 * e + 1]);
-            if (c4 == 0) { sml[2 * r] = M[e] - kWeightLog2<T>; sml[2 * r + 1] = l[e]; }
-        }
-        __syncthreads();
-        const bool whole = t0 == 0 && t1 == nt;
-        const int slot = 2 * blockIdx.x + (u == u_first ? 0 : 1);
-        for (int x = threadIdx.x; x < nh * D; x += kDecWarps * 32) {
-            const int r = x / D, col = x % D;
-            float Mx = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < kDecWarps; ++w) Mx = fmaxf(Mx, sml[2 * (w * 16 + r)]);
-            const float bs = Mx == -INFINITY ? 0.f : Mx;
-            float sum = 0.f, lsum = 0.f;
-#pragma unroll
-            for (int w = 0; w < kDecWarps; ++w) {
-                const float a = ex2(sml[2 * (w * 16 + r)] - bs);
-                sum = fmaf(a, so[(w * 16 + r) * D + col], sum);
-                lsum = fmaf(a, sml[2 * (w * 16 + r) + 1], lsum);
-            }
-            if (!bound_ok(b < p.B && h0 + r < p.H && slot < 2 * p.grid, p.word, whole ? kSiteRowOut : kSitePart)) continue;
-            if (whole) {
-                const float ov = lsum == 0.f ? 0.f : sum / lsum;
-                static_cast<T *>(p.o)[((size_t)b * p.H + h0 + r) * D + col] = T(ov);
-                if (col == 0)
-                    p.lse[(size_t)b * p.H + h0 + r] =
-                        lsum == 0.f ? -INFINITY : 0.69314718055994530942f * (bs + lg2(lsum));
-            } else {
-                p.part_o[((size_t)slot * 16 + r) * D + col] = sum;
-                if (col == 0) {
-                    p.part_ml[((size_t)slot * 16 + r) * 2] = Mx;
-                    p.part_ml[((size_t)slot * 16 + r) * 2 + 1] = lsum;
+            // one CTA had the whole group: its weights, from the logits just written
+            if (ROW && p.mass && p.nhb == 1) {
+                float *l2 = so;                                      // (the fold is done)
+                __syncthreads();
+                if (threadIdx.x < nh)
+                    l2[threadIdx.x] = p.lse[(size_t)b * p.H + h0 + threadIdx.x] * 1.4426950408889634074f;
+                __syncthreads();
+                for (int t = threadIdx.x; t < p.mass_cap; t += kDecWarps * 32) {
+                    const size_t at = ((size_t)b * p.Hk + hk) * p.mass_cap + t;
+                    float w = 0.f;
+                    if (t < n)
+                        for (int r = 0; r < nh; ++r)
+                            w += l2[r] == -INFINITY
+                                     ? 0.f
+                                     : ex2(p.logits[((size_t)b * p.H + h0 + r) * p.cap + t] - l2[r]);
+                    if (t < n || p.mass_out != p.mass) p.mass_out[at] = t < n ? p.mass[at] + w : p.mass[at];
                 }
             }
-        }
-        // one CTA had the whole group: its weights, from the logits just written
-        if (ROW && p.mass && p.nhb == 1) {
-            float *l2 = so;                                      // (the fold is done)
             __syncthreads();
-            if (threadIdx.x < nh) l2[threadIdx.x] = p.lse[(size_t)b * p.H + h0 + threadIdx.x] * 1.4426950408889634074f;
-            __syncthreads();
-            for (int t = threadIdx.x; t < p.mass_cap; t += kDecWarps * 32) {
-                const size_t at = ((size_t)b * p.Hk + hk) * p.mass_cap + t;
-                float w = 0.f;
-                if (t < n)
-                    for (int r = 0; r < nh; ++r)
-                        w += l2[r] == -INFINITY
-                                 ? 0.f
-                                 : ex2(p.logits[((size_t)b * p.H + h0 + r) * p.cap + t] - l2[r]);
-                if (t < n || p.mass_out != p.mass) p.mass_out[at] = t < n ? p.mass[at] + w : p.mass[at];
-            }
-        }
-        __syncthreads();
         }
         u = row_end;
         if constexpr (!ROW) {

@@ -77,7 +77,8 @@ __device__ __forceinline__ uint32_t weight_key(float m, bool recent) {
 // 2^31 - 1 slots, so n + page - 1 would overflow, and no page would be looked at.)
 __host__ __device__ constexpr int used_pages(int n, int page) { return n > 0 ? (n - 1) / page + 1 : 0; }
 static_assert(used_pages(0, 1) == 0 && used_pages(1, 16) == 1 && used_pages(16, 16) == 1 && used_pages(17, 16) == 2 &&
-              used_pages(2, 0x7fffffff) == 1 && used_pages(1 << 21, 0x7fffffff) == 1 && used_pages(1 << 21, 1) == 1 << 21,
+                  used_pages(2, 0x7fffffff) == 1 && used_pages(1 << 21, 0x7fffffff) == 1 &&
+                  used_pages(1 << 21, 1) == 1 << 21,
               "no sum leaves 32 bits");
 
 __global__ void __launch_bounds__(256) streamkl_evict_claim_kernel(const EvictParams p) {
@@ -455,7 +456,8 @@ __global__ void __launch_bounds__(256, 8) streamkl_evict_move_kernel(const Evict
         const unsigned td = t, fd = f;
         r += step;
         if (r < m) { t = to[r]; f = from[r]; }             // the next pair while this row travels
-        if (!bound_ok(r - step < p.list && td / (unsigned)p.page < (unsigned)p.pages && fd / (unsigned)p.page < (unsigned)p.pages,
+        if (!bound_ok(r - step < p.list && td / (unsigned)p.page < (unsigned)p.pages &&
+                          fd / (unsigned)p.page < (unsigned)p.pages,
                       p.word, kSiteSlot))
             continue;
         *reinterpret_cast<uint4 *>(row(td)) = *reinterpret_cast<const uint4 *>(row(fd));
