@@ -94,6 +94,20 @@ bool stat_shape_ok(int B, int H, int H_k, int N_Q, int N_K, int d, int dtype, in
            (double)B * H * ((N_Q + 127) / 128) * ((N_K + 127) / 128) < 1e11;      // a run's tiles are counted in 32 bits
 }
 
+// scale log2(e), with what the tensor cores leave of an fp16 logit put back.  They round the
+// running sum towards zero at each of its d / 16 additions, by half a step on average, which
+// is 0.36 2^-23 of it (the mean of step / value over a binade is 0.72 2^-23); of a sum that
+// grows evenly that comes to (d / 16 + 1) / 2 times as much.  Measured: large logits came out
+// 1.1e-7 (d = 64) and 1.5e-7 to 1.8e-7 (d = 128) too small, and with log-sum-exps from
+// elsewhere the sums' error against 64 bits was up to 7 times that of 32-bit torch (1.2e-6
+// for 1.6e-7, 1.8e-6 at most in 70 draws); with this it is 0.4 to 3 times, 1.0e-6 at most.
+// bf16 products have fewer bits to lose (0.7e-7 and 0.8e-7) and stay as they are, because
+// streamkl_fwd's log-sum-exps are off alike, so that it cancels in a weight (an error of
+// 4.6e-7 as it is, 1.3e-6 corrected).
+float fp16_scale(float scale, int d) {
+    return (float)((double)scale * 1.4426950408889634 * (1.0 + 0.36 * (d / 16 + 1) / 2 * 0x1p-23));
+}
+
 // Launch with the attributes of a dependent kernel (it may start while its
 // predecessor runs and calls grid_wait) and of a cluster, where asked for.
 template <typename K, typename... A>
@@ -300,8 +314,8 @@ streamkl_status streamkl_key_mass(const void *q, const long long *q_stride, cons
     memset(&p, 0, sizeof p);
     p.B = B; p.H = H; p.Hk = H_k; p.G = H / H_k; p.N_Q = N_Q; p.N_K = N_K; p.causal = causal;
     p.kv_len = kv_len;
-    p.c = scale * kLog2e;
     p.fp16 = dtype == kDtypeFp16;
+    p.c = p.fp16 ? fp16_scale(scale, d) : scale * kLog2e;
     p.lse = lse; p.mass = mass; p.accumulate = accumulate;
     p.part = static_cast<float *>(scratch);
     p.st.word = static_cast<uint32_t *>(workspace);

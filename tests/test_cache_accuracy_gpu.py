@@ -1,11 +1,12 @@
-"""Paged decode's products with the values: off by the output's own rounding, not by one of the weights."""
+"""Errors that are smaller than the bounds of cache_ref: decode's products with the values, off by the output's own
+rounding and not by one of the weights; fp16 logits of key mass, without a systematic part."""
 import math
 
 import pytest
 import torch
 
 import cache_ref as ref
-from attention_kl_divergence_attn_b200 import streamkl_check, streamkl_decode
+from attention_kl_divergence_attn_b200 import streamkl_check, streamkl_decode, streamkl_key_mass
 from test_cache_gpu import cache, gen, on_gpu, randn, within
 
 pytestmark = pytest.mark.gpu
@@ -75,3 +76,20 @@ def test_infinite_value(sign, dtype):
     other = torch.arange(64) != 5
     want = ref.decode(q, k, v.clamp(-100, 100), table, n, 0.1)
     within(out[..., other.cuda()], want[0][..., other], want[3][..., other], "out")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_fp16_logits_are_not_too_small(d):
+    """Key mass of single rows, lse 0: exp(y), off by the logit's error.  Its systematic part, the slope of the error
+    over y, is held to the scale's own rounding (2^-24) and a third of the correction for the tensor cores' rounding
+    towards zero: (d / 16 + 1) / 2 additions' worth of half a step, 0.36 2^-23 each."""
+    g = gen(120 + d)
+    q = randn(g, 64, 1, 1, d, dtype=FP)
+    k = (randn(g, 64, 1, 4000, d, dtype=FP).float() + q.float()).to(FP)
+    scale = float(torch.tensor(1 / math.sqrt(d), dtype=torch.float32))
+    y = (q.cuda().double() @ k.cuda().double().transpose(2, 3)).squeeze(2) * scale
+    mass, _ = streamkl_key_mass(q.cuda(), k.cuda(), torch.zeros(64, 1, 1, device="cuda"), scale)
+    assert streamkl_check() == 0
+    err = mass.double() / torch.exp(y) - 1
+    slope = float((err * y).sum() / (y * y).sum())
+    assert abs(slope) <= 2.0 ** -24 + 0.36 * (d / 16 + 1) / 2 * 2.0 ** -23 / 3, slope
