@@ -27,8 +27,8 @@
 // of the chain of dependent steps: the slots of a long sequence are spread over
 // up to 8 CTAs that add their histograms through distributed shared memory, and
 // what is kept is a bit a slot, so that ranks come from one prefix sum over the
-// words of 32 slots.  Measured: 10 us for one sequence of 1040, 19 us for 32 of
-// 4160 (8 key heads), 49 us for 4 of 32768 to 4096 (selection 22, moves 27).
+// words of 32 slots.  Measured: 11 us for one sequence of 1040, 20 us for 32 of
+// 4160 (8 key heads), 51 us for 4 of 32768 to 4096 (selection 22, moves 27).
 #pragma once
 
 #include "decode.cuh"

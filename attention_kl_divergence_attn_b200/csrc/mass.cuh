@@ -32,8 +32,9 @@
 // Work bound: one exponential a pair (16 a clock and SM: 2048 clocks a tile)
 // against 2 d flops (1024 clocks a tile at d = 128) and 32 KB of streamed rows
 // from L2 (items of 128 rows read them twice as often, 9 TB/s over all SMs).
-// Measured: 316 us for 8192 causal rows of 32 heads over 8, d = 128 (73 % of the
-// exponentials' rate); 22 us for 2 x 8 heads of 2048 rows, d = 64.
+// Measured: 338 us for 8192 causal rows of 32 heads over 8, d = 128, on inputs in
+// turn (68 % of the exponentials' rate; 318 us and 73 % on one input again and
+// again); 22 us for 2 x 8 heads of 2048 rows, d = 64.
 #pragma once
 
 #include "sm100.cuh"

@@ -343,7 +343,10 @@ streamkl_status streamkl_key_mass(const void *q, const long long *q_stride, cons
                                   void *workspace, size_t workspace_bytes, void *scratch, size_t scratch_bytes,
                                   void *stream);
 
-/* Bytes of scratch that streamkl_decode requires on the current device. */
+/* Bytes of scratch that streamkl_decode requires on the current device.  With
+ * weights that includes 4 B H cap bytes, cap being the room of a sequence: of a
+ * large table pass the columns in use (a smaller max_pages, the same
+ * table_stride). */
 size_t streamkl_decode_scratch_size(int B, int H, int H_k, int page_size, int max_pages, int d, int with_mass,
                                     int mass_cap);
 
