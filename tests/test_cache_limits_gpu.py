@@ -6,8 +6,8 @@ import torch
 
 import attention_kl_divergence_attn_b200 as skl
 import cache_ref as ref
-from attention_kl_divergence_attn_b200 import streamkl_check, streamkl_decode, streamkl_key_mass
-from test_cache_gpu import assert_evicted, gen, policy_inputs, randn
+from attention_kl_divergence_attn_b200 import streamkl_check, streamkl_decode, streamkl_evict, streamkl_key_mass
+from test_cache_gpu import assert_evicted, cache, gen, policy_inputs, randn
 
 pytestmark = pytest.mark.gpu
 BF, FP = torch.bfloat16, torch.float16
@@ -105,3 +105,42 @@ def test_key_mass_item_of_millions_of_tiles():
     want = float((times * torch.exp(0.125 * 2.0 * rows[:, 0].double())).sum())
     # a sum of 64 terms a tile half, added H N_Q / 128 times: half a step each
     assert abs(float(got[300]) - want) <= want * (2.0 ** -24 * (H * N_Q / 128 + 64) + 2.0 ** -20)
+
+
+def test_calls_from_several_threads():
+    """Host threads on streams of their own, in shapes that no other call has had: every result as from one thread."""
+    from concurrent.futures import ThreadPoolExecutor
+
+    g = gen(203)
+    sets = []
+    for i in range(4):
+        lens = (900 + 37 * i, 13 + i, 450)
+        k, v, table = cache(g, lens, 2, 64, 24 + 8 * i, BF)
+        q, qq = randn(g, 3, 6, 64), randn(g, 1, 2, 90 + i, 64)
+        n, mass = torch.tensor(lens, dtype=torch.int32), torch.rand(3, 2, table.shape[1] * (24 + 8 * i), generator=g)
+        sets.append([x.cuda() for x in (q, k.nan_to_num(0.0), v.nan_to_num(0.0), table, n, mass, qq)])
+
+    def work(x):
+        q, k, v, table, n, mass, qq = x
+        kc, vc = k.clone(), v.clone()
+        out = list(streamkl_decode(q, kc, vc, table, n, mass=mass, mass_out=(mo := torch.empty_like(mass))))
+        out += streamkl_evict(kc, vc, table, n, mo, 300)[:2]
+        out += streamkl_key_mass(qq, qq, causal=True)
+        return [*out, mo, kc, vc]
+
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+
+    def on_stream(i):
+        with torch.cuda.stream(streams[i]):
+            got = [work(sets[i]) for _ in range(30)]
+        streams[i].synchronize()
+        return got
+
+    with ThreadPoolExecutor(len(sets)) as pool:
+        many = list(pool.map(on_stream, range(len(sets))))
+    for x, got in zip(sets, many):
+        want = work(x)
+        for one in got:
+            assert all(torch.equal(a, b) for a, b in zip(one, want))
+    assert streamkl_check() == 0
